@@ -341,6 +341,109 @@ kq_status kq_last_device_error(const kq_layer_desc *desc, void *act, int32_t M,
 kq_status kq_debug_wait_timeout(const kq_layer_desc *desc, void *act, int32_t M,
                                 uint32_t limit_us, kq_stream_t stream);
 
+/* ---------------------------------------------------------------------------------
+ * 8-bit operators: a linear layer, its gated form and the root-mean-square norm in front
+ * of them, with E4M3 codes and one power-of-two scale for each block of 128. They serve
+ * the layers that do not stand 4 bits, and the feed-forward blocks of language models.
+ *
+ * Format. An activation block is 128 consecutive features of one token, a weight block a
+ * 128 x 128 piece of W; a last block may be shorter. A block's scale is 2^e (E8M0 byte
+ * e + 127) with e the smallest exponent >= -127 for which no value of it exceeds
+ * 448 * 2^e, so nothing saturates; a block of zeros has byte 0. Codes are value * 2^-e
+ * rounded to the nearest E4M3, ties to even. A block that holds an infinity or a NaN has
+ * byte 0xFF and NaN codes, and every output that it enters is NaN.
+ * The product is exact in the codes: the tensor cores apply the powers of two and
+ * accumulate in fp32.
+ *
+ * Matrices are row-major; ldx, ldr, ldy are row pitches in elements (at least the width,
+ * rows a multiple of 16 bytes apart). K % 32 == 0, N % 16 == 0, M >= 1. Conventions for
+ * ownership, streams, errors and alignment are those at the top of this file. Calls that
+ * may run at the same time need workspaces of their own.
+ * ------------------------------------------------------------------------------- */
+typedef enum { KQ_ACT_SILU = 0, KQ_ACT_GELU = 1 } kq_activation;
+
+/* One 8-bit layer. gated == 0: Y = X W, W [K, N]. gated == 1: two matrices of that shape
+ * and Y = act(X Wgate) * (X Wup), act SiLU  z / (1 + e^-z)  or GELU in its erf form. */
+typedef struct {
+  int32_t K;             /* input features, K % 32 == 0 */
+  int32_t N;             /* output features, N % 16 == 0 */
+  int32_t gated;         /* 0 or 1 */
+  int32_t activation;    /* kq_activation, used when gated */
+} kq_fp8_desc;
+
+/* Bytes of the prepared weights, and of the activation workspace for M tokens of K features
+ * (codes, scales, the device error word). 0 for invalid arguments. */
+size_t kq_fp8_weights_bytes(const kq_fp8_desc *desc);
+size_t kq_fp8_act_bytes(int32_t K, int32_t M);
+
+/* Quantizes W_bf16 [K, N] (gated: and Wup_bf16 [K, N], else null), bf16 on the device, into
+ * `weights` (kq_fp8_weights_bytes). Async on `stream`. */
+kq_status kq_fp8_prepare_weights(const kq_fp8_desc *desc, const void *W_bf16, const void *Wup_bf16,
+                                 void *weights, kq_stream_t stream);
+
+/* Canonical parts <-> prepared weights, all on the device: codes uint8 (E4M3) [N, K], scales
+ * uint8 (E8M0) [ceil(N / 128), ceil(K / 128)], the up_ pair for gated layers only. Unpacking
+ * skips null parts. */
+kq_status kq_fp8_weights_pack(const kq_fp8_desc *desc, const void *codes, const void *scales,
+                              const void *up_codes, const void *up_scales, void *weights,
+                              kq_stream_t stream);
+kq_status kq_fp8_weights_unpack(const kq_fp8_desc *desc, const void *weights, void *codes,
+                                void *scales, void *up_codes, void *up_scales, kq_stream_t stream);
+
+/* Quantizes X (bf16 [M, K], pitch ldx) into an activation workspace. */
+kq_status kq_fp8_quantize_act(int32_t K, const void *X_bf16, int64_t ldx, int32_t M, void *act,
+                              size_t act_bytes, kq_stream_t stream);
+
+/* The root-mean-square norm with the residual's addition and an 8-bit output, per token:
+ *   h = x + residual     one fp32 sum, rounded to the residual's type (residual_dtype:
+ *                        KQ_OUT_BF16 or KQ_OUT_F32) and written back to `residual`;
+ *                        h = x where residual is null (ldr and residual_dtype are ignored)
+ *   r = 1 / sqrt(mean_k h_k^2 + eps)    in float64, rounded once to fp32
+ *   y = (h * r) * gamma                 two fp32 products, quantized into `act`
+ * gamma: device, fp32 [K]; eps > 0; K <= 32768 (else KQ_ERR_UNSUPPORTED_SHAPE). X and
+ * residual may be the same buffer only if they are the same matrix. */
+kq_status kq_fp8_rmsnorm_act(int32_t K, const void *X_bf16, int64_t ldx, void *residual, int64_t ldr,
+                             int32_t residual_dtype, const float *gamma, float eps, int32_t M,
+                             void *act, size_t act_bytes, kq_stream_t stream);
+
+/* Canonical parts <-> activation workspace, all on the device: codes uint8 [M, K], scales
+ * uint8 [M, ceil(K / 128)]. Unpacking skips null parts; `values` [M, K] (contiguous, 16-byte
+ * aligned, bf16 or fp32 per values_dtype) receives code * 2^e. */
+kq_status kq_fp8_act_pack(int32_t K, const void *codes, const void *scales, int32_t M, void *act,
+                          size_t act_bytes, kq_stream_t stream);
+kq_status kq_fp8_act_unpack(int32_t K, const void *act, int32_t M, void *codes, void *scales,
+                            void *values, int32_t values_dtype, kq_stream_t stream);
+
+/* The layer on a filled activation workspace: Y [M, N] (pitch ldy, KQ_OUT_F32 or
+ * KQ_OUT_BF16). Rows past M and columns past N are left as they were. */
+kq_status kq_fp8_gemm(const kq_fp8_desc *desc, const void *weights, void *act, int32_t M, void *Y,
+                      int64_t ldy, int32_t out_dtype, kq_stream_t stream);
+
+/* A gated layer whose output is quantized into out_act, the activation workspace
+ * (kq_fp8_act_bytes(N, M)) of a following layer with N input features; N % 32 == 0. */
+kq_status kq_fp8_gated_act(const kq_fp8_desc *desc, const void *weights, void *act, int32_t M,
+                           void *out_act, size_t out_act_bytes, kq_stream_t stream);
+
+/* kq_fp8_quantize_act, then kq_fp8_gemm. */
+kq_status kq_fp8_linear(const kq_fp8_desc *desc, const void *weights, const void *X_bf16, int64_t ldx,
+                        int32_t M, void *Y, int64_t ldy, int32_t out_dtype, void *act,
+                        size_t act_bytes, kq_stream_t stream);
+
+/* A feed-forward block, Y = (act(y Wgate) * (y Wup)) Wdown: kq_fp8_rmsnorm_act (gamma null:
+ * kq_fp8_quantize_act, and no residual), kq_fp8_gated_act with `gated`, kq_fp8_gemm with
+ * `down` (not gated, down->K == gated->N). ws: kq_fp8_ffn_bytes bytes (0 for invalid
+ * arguments); it starts with the workspace kq_fp8_last_device_error takes. */
+size_t kq_fp8_ffn_bytes(const kq_fp8_desc *gated, const kq_fp8_desc *down, int32_t M);
+kq_status kq_fp8_ffn(const kq_fp8_desc *gated, const void *gated_weights, const kq_fp8_desc *down,
+                     const void *down_weights, const void *X_bf16, int64_t ldx, void *residual,
+                     int64_t ldr, int32_t residual_dtype, const float *gamma, float eps, int32_t M,
+                     void *Y, int64_t ldy, int32_t out_dtype, void *ws, size_t ws_bytes,
+                     kq_stream_t stream);
+
+/* Synchronises `stream`, reports (KQ_ERR_DEVICE_TIMEOUT or KQ_OK) and clears the error word
+ * of an 8-bit workspace. A call that fills the workspace clears it too. */
+kq_status kq_fp8_last_device_error(void *act, kq_stream_t stream);
+
 /* Static string for a status code. */
 const char *kq_status_string(kq_status s);
 

@@ -1,0 +1,452 @@
+"""GPU: the 8-bit operators against the float64 oracle.
+
+Codes and scales are compared bit for bit (both sides decide them from the same float32 values).
+Products: the decoded operands are exact in float64 and each product of two codes is exact in the
+tensor core, so a result may be off by the fp32 accumulation alone: one rounding (or truncation,
+2^-23 of the running sum) for each 32-element step, K / 32 of them, plus the final rounding of
+the output type. The running sum is at most sum |a||b|.
+"""
+import numpy as np
+import pytest
+
+from oracle import fp8
+
+pytestmark = pytest.mark.gpu
+
+EPS = 1e-6
+
+
+def _t(a, dtype=None):
+    import torch
+    t = torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    return t if dtype is None else t.to(dtype)
+
+
+def _bf16(a):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).to(torch.bfloat16)
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+def tokens(M, K, seed):
+    """bf16 rows of very different sizes with a few large channels."""
+    rng = np.random.default_rng(seed)
+    x = rng.standard_normal((M, K)) * np.exp(2 * rng.standard_normal((M, 1)))
+    x[:, rng.integers(0, K, max(1, K // 200))] *= 20
+    return _bf16(x)
+
+
+def weight(K, N, seed):
+    """bf16 [K, N] whose 128 x 128 pieces have scales of their own."""
+    rng = np.random.default_rng(seed + 77)
+    w = rng.standard_normal((K, N)) / np.sqrt(K)
+    w *= np.repeat(np.repeat(np.exp2(rng.integers(-3, 4, (-(-K // 128), -(-N // 128)))), 128, 0), 128, 1)[:K, :N]
+    return _bf16(w)
+
+
+def buf(n):
+    import torch
+    return torch.zeros(n, dtype=torch.uint8, device="cuda")
+
+
+def unpack(kq, act, M, K):
+    c, s = buf(M * K), buf(M * -(-K // 128))
+    kq.fp8_act_unpack(K, act, M, c, s)
+    return c.cpu().numpy().reshape(M, K), s.cpu().numpy().reshape(M, -1)
+
+
+def packed(kq, L, W, Wu=None):
+    """Prepared weights and the decoded [N, K] values of each matrix."""
+    w = buf(kq.fp8_weights_bytes(L))
+    enc = [fp8.encode_weight(_np(m)) for m in (W, Wu) if m is not None]
+    parts = [_t(a) for e in enc for a in e]
+    kq.fp8_weights_pack(L, parts[0], parts[1], w, *parts[2:])
+    return w, [fp8.decode_weight(*e) for e in enc]
+
+
+def accumulation(A, W):
+    """Bound on the fp32 accumulation error of A W^T (see the module's docstring)."""
+    return (A.shape[1] / 32 + 2) * 2.0 ** -23 * (np.abs(A) @ np.abs(W).T)
+
+
+HALF = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
+
+
+# ------------------------------------------------------------------------------ codes ----
+@pytest.mark.parametrize("M,K", [(1, 32), (3, 96), (130, 128), (7, 160), (33, 1152), (2, 2080), (1, 4096), (5, 8224),
+                                 (2, 36864)])
+def test_quantize_bit_exact(cuda_device, M, K):
+    import torch
+    import w4a4_post_quantization_token_b200 as kq
+    X = tokens(M, K, M + K)
+    X[0, :32] = 0
+    act = buf(kq.fp8_act_bytes(K, M))
+    kq.fp8_quantize_act(X.cuda(), act)
+    c, s = unpack(kq, act, M, K)
+    rc, rs = fp8.encode_rows(_np(X))
+    np.testing.assert_array_equal(s, rs)
+    np.testing.assert_array_equal(c, rc)
+    for dt in (torch.bfloat16, torch.float32):
+        v = torch.empty(M, K, dtype=dt, device="cuda")
+        kq.fp8_act_unpack(K, act, M, values=v)
+        np.testing.assert_array_equal(_np(v), fp8.decode_rows(rc, rs))
+    # and back through the canonical parts
+    act2 = buf(kq.fp8_act_bytes(K, M))
+    kq.fp8_act_pack(K, _t(rc), _t(rs), M, act2)
+    c2, s2 = unpack(kq, act2, M, K)
+    np.testing.assert_array_equal(c2, rc)
+    np.testing.assert_array_equal(s2, rs)
+
+
+def test_quantize_every_bf16_magnitude(cuda_device):
+    """Rows that hold every finite bf16 pattern, each beside a maximum of its own exponent."""
+    import torch
+    import w4a4_post_quantization_token_b200 as kq
+    bits = np.arange(0x7F80, dtype=np.uint16)
+    bits = np.concatenate([bits, bits | 0x8000])
+    K = 128
+    bits = np.resize(bits, (-(-bits.size // K)) * K).reshape(-1, K)
+    X = torch.from_numpy(bits.view(np.int16).copy()).view(torch.bfloat16)
+    act = buf(kq.fp8_act_bytes(K, X.shape[0]))
+    kq.fp8_quantize_act(X.cuda(), act)
+    c, s = unpack(kq, act, X.shape[0], K)
+    rc, rs = fp8.encode_rows(_np(X))
+    np.testing.assert_array_equal(s, rs)
+    np.testing.assert_array_equal(c, rc)
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_non_finite_blocks_are_nan(cuda_device, bad):
+    import torch
+    import w4a4_post_quantization_token_b200 as kq
+    M, K, N = 4, 320, 32
+    X = tokens(M, K, 3)
+    X[1, 200] = bad
+    act = buf(kq.fp8_act_bytes(K, M))
+    kq.fp8_quantize_act(X.cuda(), act)
+    c, s = unpack(kq, act, M, K)
+    rc, rs = fp8.encode_rows(_np(X))
+    np.testing.assert_array_equal(s, rs)
+    np.testing.assert_array_equal(c, rc)
+    L = kq.Fp8Layer(K, N)
+    w, (Wd,) = packed(kq, L, weight(K, N, 0))
+    Y = torch.zeros(M, N, device="cuda")
+    kq.fp8_gemm(L, w, act, M, Y)
+    y = _np(Y)
+    assert np.all(np.isnan(y[1])) and np.all(np.isfinite(y[[0, 2, 3]]))
+
+
+@pytest.mark.parametrize("K,N", [(32, 16), (128, 128), (160, 144), (1152, 400), (96, 1040)])
+def test_prepare_weights_bit_exact(cuda_device, K, N):
+    import w4a4_post_quantization_token_b200 as kq
+    W, Wu = weight(K, N, 1), weight(K, N, 2)
+    L = kq.Fp8Layer(K, N, gated=True)
+    w = buf(kq.fp8_weights_bytes(L))
+    kq.fp8_prepare_weights(L, W.cuda(), w, Wu.cuda())
+    ns = -(-N // 128) * -(-K // 128)
+    got = [buf(N * K), buf(ns), buf(N * K), buf(ns)]
+    kq.fp8_weights_unpack(L, w, *got)
+    for m, c, s in ((W, got[0], got[1]), (Wu, got[2], got[3])):
+        rc, rs = fp8.encode_weight(_np(m))
+        np.testing.assert_array_equal(c.cpu().numpy().reshape(N, K), rc)
+        np.testing.assert_array_equal(s.cpu().numpy().reshape(rs.shape), rs)
+    w2 = buf(kq.fp8_weights_bytes(L))
+    kq.fp8_weights_pack(L, got[0], got[1], w2, got[2], got[3])
+    got2 = [buf(N * K), buf(ns), buf(N * K), buf(ns)]
+    kq.fp8_weights_unpack(L, w2, *got2)
+    for a, b in zip(got, got2):
+        np.testing.assert_array_equal(a.cpu().numpy(), b.cpu().numpy())
+
+
+# ------------------------------------------------------------------------------- norm ----
+@pytest.mark.parametrize("res", [None, "bf16", "f32"])
+@pytest.mark.parametrize("M,K", [(1, 32), (5, 160), (130, 1152), (3, 4096), (2, 6176), (2, 12288), (1, 32768)])
+def test_rmsnorm_bit_exact(cuda_device, M, K, res):
+    import torch
+    import w4a4_post_quantization_token_b200 as kq
+    rng = np.random.default_rng(K + M)
+    X = tokens(M, K, K)
+    X[0, :64] = 0
+    gamma = (1 + 0.25 * rng.standard_normal(K)).astype(np.float32)
+    R = round_ = None
+    if res:
+        R = torch.from_numpy(3 * rng.standard_normal((M, K)).astype(np.float32))
+        R = R.to(torch.bfloat16) if res == "bf16" else R
+        round_ = (lambda h: torch.from_numpy(h).to(torch.bfloat16).float().numpy()) if res == "bf16" else None
+    act = buf(kq.fp8_act_bytes(K, M))
+    Rg = None if R is None else R.clone().cuda()
+    kq.fp8_rmsnorm_act(X.cuda(), _t(gamma), EPS, act, residual=Rg)
+    y, h = fp8.rmsnorm(_np(X), gamma, EPS, None if R is None else _np(R), round_)
+    rc, rs = fp8.encode_rows(y)
+    c, s = unpack(kq, act, M, K)
+    if res:
+        np.testing.assert_array_equal(_np(Rg), h.astype(np.float64))
+    np.testing.assert_array_equal(s, rs)
+    np.testing.assert_array_equal(c, rc)
+
+
+def test_rmsnorm_zero_and_overflowing_rows(cuda_device):
+    """A row of zeros stays zero; a sum that leaves bf16 makes its row NaN and no other."""
+    import torch
+    import w4a4_post_quantization_token_b200 as kq
+    M, K = 3, 256
+    X = tokens(M, K, 9)
+    X[0] = 0
+    R = torch.zeros(M, K, dtype=torch.bfloat16)
+    X[1, 5] = R[1, 5] = 3e38
+    act = buf(kq.fp8_act_bytes(K, M))
+    Rg = R.cuda()
+    kq.fp8_rmsnorm_act(X.cuda(), torch.ones(K, device="cuda"), EPS, act, residual=Rg)
+    c, s = unpack(kq, act, M, K)
+    assert np.all(c[0] == 0) and np.all(s[0] == 0)
+    assert np.isinf(_np(Rg)[1, 5]) and s[1, 0] == 0xFF
+    assert not np.any(s[2] == 0xFF)
+
+
+def test_pitched_rows_and_untouched_neighbours(cuda_device):
+    """X, the residual and Y as column slices of wider tensors; nothing outside is written."""
+    import torch
+    import w4a4_post_quantization_token_b200 as kq
+    M, K, N = 37, 160, 144
+    wide = torch.full((M + 3, K + 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    X = tokens(M, K, 1).cuda()
+    wide[:M, 16:16 + K] = X
+    R = torch.randn(M, K)
+    wr = torch.full((M + 3, K + 32), 5.0, device="cuda")
+    wr[:M, 8:8 + K] = R.cuda()
+    gamma = torch.rand(K, device="cuda")
+    a, b = buf(kq.fp8_act_bytes(K, M)), buf(kq.fp8_act_bytes(K, M))
+    Rc = R.cuda()
+    kq.fp8_rmsnorm_act(X, gamma, EPS, a, residual=Rc)
+    kq.fp8_rmsnorm_act(wide[:M, 16:16 + K], gamma, EPS, b, residual=wr[:M, 8:8 + K])
+    for u, v in zip(unpack(kq, a, M, K), unpack(kq, b, M, K)):
+        np.testing.assert_array_equal(u, v)
+    np.testing.assert_array_equal(_np(wr[:M, 8:8 + K]), _np(Rc))
+    assert torch.all(wr[M:] == 5) and torch.all(wr[:, :8] == 5) and torch.all(wr[:, 8 + K:] == 5)
+    L = kq.Fp8Layer(K, N)
+    w, _ = packed(kq, L, weight(K, N, 4))
+    for dt, flag, M2 in ((torch.float32, kq.OUT_F32, M), (torch.bfloat16, kq.OUT_BF16, M), (torch.bfloat16, kq.OUT_BF16, 300)):
+        X2 = tokens(M2, K, 2).cuda()
+        act = buf(kq.fp8_act_bytes(K, M2))
+        Y = torch.empty(M2, N, dtype=dt, device="cuda")
+        wy = torch.full((M2 + 5, N + 48), 3.0, dtype=dt, device="cuda")
+        kq.fp8_linear(L, w, X2, Y, act, flag)
+        kq.fp8_linear(L, w, X2, wy[:M2, 16:16 + N], act, flag)
+        assert torch.equal(wy[:M2, 16:16 + N], Y)
+        assert torch.all(wy[M2:] == 3) and torch.all(wy[:, :16] == 3) and torch.all(wy[:, 16 + N:] == 3)
+
+
+# --------------------------------------------------------------------------- products ----
+SHAPES = [(1, 32, 16), (1, 4096, 256), (3, 96, 48), (16, 512, 128), (17, 544, 144), (32, 1152, 272), (33, 128, 400),
+          (64, 640, 128), (65, 2080, 256), (127, 160, 272), (128, 384, 128), (129, 1024, 144), (200, 12288, 160),
+          (257, 1152, 528), (300, 96, 1040), (520, 736, 784), (1, 12288, 1040), (5, 8192, 640)]
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("M,K,N", SHAPES)
+def test_linear(cuda_device, M, K, N, out):
+    import torch
+    import w4a4_post_quantization_token_b200 as kq
+    X, W = tokens(M, K, K + N), weight(K, N, M)
+    L = kq.Fp8Layer(K, N)
+    w, (Wd,) = packed(kq, L, W)
+    act = buf(kq.fp8_act_bytes(K, M))
+    Y = torch.full((M, N), float("nan"), dtype=torch.bfloat16 if out == "bf16" else torch.float32, device="cuda")
+    kq.fp8_linear(L, w, X.cuda(), Y, act, kq.OUT_BF16 if out == "bf16" else kq.OUT_F32)
+    assert kq.fp8_last_device_error(act) == 0
+    A = fp8.decode_rows(*fp8.encode_rows(_np(X)))
+    ref = A @ Wd.T
+    acc = accumulation(A, Wd)
+    assert np.all(np.abs(_np(Y) - ref) <= HALF[out] * (np.abs(ref) + acc) + acc + 1e-37)
+
+
+def gated_bound(z, u, zerr, uerr, kind):
+    """|act'| <= 1.13 (GELU; SiLU 1.10) and fp32 evaluation of act within 2^-19 of |act| (exp and
+    the quotient a few ulps, the exponent's rounding 2^-24 |z| log2 e with |z| <= 20 before act
+    leaves the linear range)."""
+    a = np.abs(fp8.activation(z, kind))
+    return 1.13 * zerr * (np.abs(u) + uerr) + a * uerr + 2.0 ** -19 * a * np.abs(u)
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+@pytest.mark.parametrize("M,K,N", [(1, 32, 16), (2, 4096, 128), (16, 160, 144), (20, 512, 272), (64, 1152, 256),
+                                   (65, 96, 400), (130, 2080, 272), (300, 640, 528), (1, 8192, 640)])
+def test_gated(cuda_device, M, K, N, kind):
+    import torch
+    import w4a4_post_quantization_token_b200 as kq
+    X, W, Wu = tokens(M, K, K), weight(K, N, 1), weight(K, N, 2)
+    L = kq.Fp8Layer(K, N, gated=True, activation=kind)
+    w, (Wd, Wud) = packed(kq, L, W, Wu)
+    act = buf(kq.fp8_act_bytes(K, M))
+    A = fp8.decode_rows(*fp8.encode_rows(_np(X)))
+    z, u = A @ Wd.T, A @ Wud.T
+    ref = fp8.activation(z, kind) * u
+    bound = gated_bound(z, u, accumulation(A, Wd), accumulation(A, Wud), kind)
+    for out, dt, flag in (("f32", torch.float32, kq.OUT_F32), ("bf16", torch.bfloat16, kq.OUT_BF16)):
+        Y = torch.full((M, N), float("nan"), dtype=dt, device="cuda")
+        kq.fp8_linear(L, w, X.cuda(), Y, act, flag)
+        assert kq.fp8_last_device_error(act) == 0
+        assert np.all(np.abs(_np(Y) - ref) <= HALF[out] * (np.abs(ref) + bound) + bound + 1e-37)
+    if N % 32:
+        return
+    # 8-bit output: half a step of the E4M3 grid under the block's own scale, which holds the
+    # block's largest value and is no larger than it needs to be
+    h = buf(kq.fp8_act_bytes(N, M))
+    kq.fp8_gated_act(L, w, act, M, h)
+    c, s = unpack(kq, h, M, N)
+    scale = np.repeat(np.ldexp(1.0, s.astype(int) - 127), 128, 1)[:, :N]
+    got = fp8.decode_rows(c, s)
+    assert np.all(np.abs(got - ref) <= 2.0 ** -4 * (np.abs(ref) + bound) + 2.0 ** -10 * scale + bound)
+    pad = np.zeros((M, s.shape[1] * 128))
+    for sign in (1, -1):
+        pad[:, :N] = np.abs(ref) + sign * bound
+        top = pad.reshape(M, -1, 128).max(2)
+        e = np.array([fp8.exponent_of(t) if t > 0 else -127 for t in top.ravel()]).reshape(top.shape) + 127
+        assert np.all(s <= e) if sign == 1 else np.all(s >= e)
+
+
+# ------------------------------------------------------------------- the block, whole ----
+def make_ffn(kq, K, N, seed=0):
+    G, D = kq.Fp8Layer(K, N, gated=True), kq.Fp8Layer(N, K)
+    gw, (Wg, Wu) = packed(kq, G, weight(K, N, seed), weight(K, N, seed + 1))
+    dw, (Wd,) = packed(kq, D, weight(N, K, seed + 2))
+    return G, gw, D, dw, Wg, Wu, Wd
+
+
+@pytest.mark.parametrize("res", [None, "bf16", "f32"])
+@pytest.mark.parametrize("M,K,N", [(1, 256, 512), (9, 1152, 608), (100, 160, 288), (260, 512, 1056)])
+def test_ffn_is_its_parts(cuda_device, M, K, N, res):
+    """The block gives what its three calls give, bit for bit, and is near the float64 chain."""
+    import torch
+    import w4a4_post_quantization_token_b200 as kq
+    G, gw, D, dw, Wg, Wu, Wd = make_ffn(kq, K, N)
+    X = tokens(M, K, 5)
+    gamma = torch.rand(K) + 0.5
+    R = None if res is None else torch.randn(M, K).to(torch.bfloat16 if res == "bf16" else torch.float32)
+    R1, R2 = (None, None) if R is None else (R.clone().cuda(), R.clone().cuda())
+    ws = buf(kq.fp8_ffn_bytes(G, D, M))
+    Y = torch.empty(M, K, device="cuda")
+    kq.fp8_ffn(G, gw, D, dw, X.cuda(), gamma.cuda(), EPS, Y, ws, residual=R1)
+    assert kq.fp8_last_device_error(ws) == 0
+    a, h = buf(kq.fp8_act_bytes(K, M)), buf(kq.fp8_act_bytes(N, M))
+    Y2 = torch.empty(M, K, device="cuda")
+    kq.fp8_rmsnorm_act(X.cuda(), gamma.cuda(), EPS, a, residual=R2)
+    kq.fp8_gated_act(G, gw, a, M, h)
+    kq.fp8_gemm(D, dw, h, M, Y2)
+    assert torch.equal(Y, Y2) and (R is None or torch.equal(R1, R2))
+    round_ = (lambda v: torch.from_numpy(v).to(torch.bfloat16).float().numpy()) if res == "bf16" else None
+    y, _ = fp8.rmsnorm(_np(X), gamma.numpy(), EPS, None if R is None else _np(R), round_)
+    A = fp8.decode_rows(*fp8.encode_rows(y))
+    H = fp8.gated(A, Wg, Wu)
+    ref = fp8.decode_rows(*fp8.encode_rows(H)) @ Wd.T
+    # H is off by d = (K / 32) 2^-23 or so; a share 2 d / 2^-4 of its codes sits that close to a
+    # border and moves by a step of 2^-3: sqrt(32 d) / 8 relative, at most 4e-3 for K = 1152
+    d = (K / 32 + 8) * 2.0 ** -23
+    err = np.linalg.norm(_np(Y) - ref) / np.linalg.norm(ref)
+    assert err <= np.sqrt(32 * d) / 8 + 1e-6
+
+
+def test_ffn_without_norm(cuda_device):
+    import torch
+    import w4a4_post_quantization_token_b200 as kq
+    M, K, N = 21, 256, 160
+    G, gw, D, dw, *_ = make_ffn(kq, K, N)
+    X = tokens(M, K, 6).cuda()
+    ws = buf(kq.fp8_ffn_bytes(G, D, M))
+    Y, Y2 = (torch.empty(M, K, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    kq.fp8_ffn(G, gw, D, dw, X, None, EPS, Y, ws, kq.OUT_BF16)
+    a, h = buf(kq.fp8_act_bytes(K, M)), buf(kq.fp8_act_bytes(N, M))
+    kq.fp8_quantize_act(X, a)
+    kq.fp8_gated_act(G, gw, a, M, h)
+    kq.fp8_gemm(D, dw, h, M, Y2, kq.OUT_BF16)
+    assert torch.equal(Y, Y2)
+
+
+@pytest.mark.parametrize("M", [1, 40, 600])
+def test_graph_replay_and_side_stream(cuda_device, M):
+    """A captured block replays on new inputs; a block on another stream gives the same."""
+    import torch
+    import w4a4_post_quantization_token_b200 as kq
+    K, N = 512, 544
+    G, gw, D, dw, *_ = make_ffn(kq, K, N)
+    gamma = torch.rand(K, device="cuda")
+    X, R = tokens(M, K, 1).cuda(), torch.randn(M, K, device="cuda")
+    X0, R0 = X.clone(), R.clone()
+    ws = buf(kq.fp8_ffn_bytes(G, D, M))
+    Y = torch.empty(M, K, device="cuda")
+    kq.fp8_ffn(G, gw, D, dw, X, gamma, EPS, Y, ws, residual=R)
+    torch.cuda.synchronize()
+    want, wantR = Y.clone(), R.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        kq.fp8_ffn(G, gw, D, dw, X, gamma, EPS, Y, ws, residual=R)
+    for k in range(3):
+        X2, R2 = tokens(M, K, 10 + k).cuda(), torch.randn(M, K, device="cuda")
+        X.copy_(X2); R.copy_(R2)
+        g.replay()
+        Ye, Re, wse = torch.empty_like(Y), R2.clone(), buf(ws.numel())
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        kq.fp8_ffn(G, gw, D, dw, X2, gamma, EPS, Ye, wse, residual=Re, stream=s)
+        torch.cuda.current_stream().wait_stream(s)
+        torch.cuda.synchronize()
+        assert torch.equal(Y, Ye) and torch.equal(R, Re)
+    X.copy_(X0); R.copy_(R0)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(Y, want) and torch.equal(R, wantR)
+
+
+def test_calls_follow_one_another(cuda_device):
+    """Many dependent calls on the same buffers without a wait between them."""
+    import torch
+    import w4a4_post_quantization_token_b200 as kq
+    K = N = 512
+    L = kq.Fp8Layer(K, N)
+    w, _ = packed(kq, L, weight(K, N, 3))
+    outs = []
+    for wait in (True, False):
+        X = tokens(24, K, 8).cuda()
+        act = buf(kq.fp8_act_bytes(K, 24))
+        Y = torch.empty(24, N, dtype=torch.bfloat16, device="cuda")
+        for _ in range(30):
+            kq.fp8_linear(L, w, X, Y, act, kq.OUT_BF16)
+            X, Y = Y, X
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        outs.append(X.clone())
+    assert torch.equal(*outs) and torch.isfinite(outs[0].float()).all()
+
+
+def test_repacked_weights_are_read_at_once(cuda_device):
+    """New weights written into the same buffer directly before a call are the ones it uses."""
+    import torch
+    import w4a4_post_quantization_token_b200 as kq
+    M, K, N = 8, 1024, 512
+    L = kq.Fp8Layer(K, N)
+    X = tokens(M, K, 2).cuda()
+    act = buf(kq.fp8_act_bytes(K, M))
+    parts = [[_t(a) for a in fp8.encode_weight(_np(weight(K, N, s)))] for s in (1, 2)]
+    want = []
+    for p in parts:
+        w = buf(kq.fp8_weights_bytes(L))
+        kq.fp8_weights_pack(L, *p, w)
+        torch.cuda.synchronize()
+        Y = torch.empty(M, N, device="cuda")
+        kq.fp8_linear(L, w, X, Y, act)
+        want.append(Y)
+    w = buf(kq.fp8_weights_bytes(L))
+    for _ in range(10):
+        for p, y in zip(parts, want):
+            Y = torch.empty(M, N, device="cuda")
+            kq.fp8_weights_pack(L, *p, w)
+            kq.fp8_gemm(L, w, act, M, Y)
+            Y2 = torch.empty(M, N, device="cuda")
+            kq.fp8_weights_pack(L, *p, w)
+            kq.fp8_linear(L, w, X, Y2, act)
+            torch.cuda.synchronize()
+            assert torch.equal(Y, y) and torch.equal(Y2, y)

@@ -20,13 +20,19 @@ __all__ = ["KQError", "Layer", "lib", "library_path", "weights_bytes", "act_byte
            "gemm", "weights_pack", "weights_unpack", "act_pack", "act_unpack",
            "debug_transform", "debug_encode_f32", "debug_wait_timeout", "last_device_error",
            "status_string", "ERR_DEVICE_TIMEOUT", "ERR_LOWRANK_RANGE",
-           "OUT_F32", "OUT_BF16", "SYMBOLS"]
+           "OUT_F32", "OUT_BF16", "SYMBOLS",
+           "Fp8Layer", "fp8_weights_bytes", "fp8_act_bytes", "fp8_ffn_bytes",
+           "fp8_prepare_weights", "fp8_weights_pack", "fp8_weights_unpack", "fp8_quantize_act",
+           "fp8_rmsnorm_act", "fp8_act_pack", "fp8_act_unpack", "fp8_gemm", "fp8_gated_act",
+           "fp8_linear", "fp8_ffn", "fp8_last_device_error", "ACT_SILU", "ACT_GELU"]
 
 OUT_F32, OUT_BF16 = 0, 1
 ERR_DEVICE_TIMEOUT, ERR_LOWRANK_RANGE = 7, 9
 T_NONE, T_KRON, T_RPBH = 0, 1, 2
 _KIND = {"none": T_NONE, "kron": T_KRON, "rpbh": T_RPBH}
 CB_MXFP4, CB_LLOYDMAX = 0, 1
+ACT_SILU, ACT_GELU = 0, 1
+_ACTIVATION = {"silu": ACT_SILU, "gelu": ACT_GELU}
 _CODEBOOK = {"mxfp4": CB_MXFP4, "lloydmax": CB_LLOYDMAX}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -38,7 +44,12 @@ SYMBOLS = ["kq_weights_bytes", "kq_act_bytes", "kq_prepare_ws_bytes", "kq_prepar
            "kq_weights_unpack", "kq_act_pack", "kq_act_unpack", "kq_debug_transform",
            "kq_debug_encode_f32", "kq_last_device_error", "kq_status_string", "kq_version",
            "kq_linear_noalloc", "kq_smooth_quantize_act", "kq_prepare_weights_lp",
-           "kq_debug_encode_lp_f32", "kq_lloydmax_codebook", "kq_debug_wait_timeout"]
+           "kq_debug_encode_lp_f32", "kq_lloydmax_codebook", "kq_debug_wait_timeout",
+           "kq_fp8_weights_bytes", "kq_fp8_act_bytes", "kq_fp8_ffn_bytes",
+           "kq_fp8_prepare_weights", "kq_fp8_weights_pack", "kq_fp8_weights_unpack",
+           "kq_fp8_quantize_act", "kq_fp8_rmsnorm_act", "kq_fp8_act_pack", "kq_fp8_act_unpack",
+           "kq_fp8_gemm", "kq_fp8_gated_act", "kq_fp8_linear", "kq_fp8_ffn",
+           "kq_fp8_last_device_error"]
 
 
 class KQError(RuntimeError):
@@ -71,8 +82,15 @@ class _LayerDesc(ctypes.Structure):
                 ("codebook", ctypes.c_int32)]
 
 
+class _Fp8Desc(ctypes.Structure):
+    _fields_ = [("K", ctypes.c_int32), ("N", ctypes.c_int32), ("gated", ctypes.c_int32),
+                ("activation", ctypes.c_int32)]
+
+
 _P = ctypes.c_void_p
 _D = ctypes.POINTER(_LayerDesc)
+_F = ctypes.POINTER(_Fp8Desc)
+_I32, _I64, _SZ = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _sigs = {
     "kq_weights_bytes": (ctypes.c_size_t, [_D]),
     "kq_act_bytes": (ctypes.c_size_t, [_D, ctypes.c_int32]),
@@ -100,6 +118,23 @@ _sigs = {
     "kq_lloydmax_codebook": (ctypes.c_int, [_P, _P]),
     "kq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "kq_version": (ctypes.c_char_p, []),
+    "kq_fp8_weights_bytes": (_SZ, [_F]),
+    "kq_fp8_act_bytes": (_SZ, [_I32, _I32]),
+    "kq_fp8_ffn_bytes": (_SZ, [_F, _F, _I32]),
+    "kq_fp8_prepare_weights": (ctypes.c_int, [_F, _P, _P, _P, _P]),
+    "kq_fp8_weights_pack": (ctypes.c_int, [_F, _P, _P, _P, _P, _P, _P]),
+    "kq_fp8_weights_unpack": (ctypes.c_int, [_F, _P, _P, _P, _P, _P, _P]),
+    "kq_fp8_quantize_act": (ctypes.c_int, [_I32, _P, _I64, _I32, _P, _SZ, _P]),
+    "kq_fp8_rmsnorm_act": (ctypes.c_int, [_I32, _P, _I64, _P, _I64, _I32, _P, ctypes.c_float, _I32,
+                                          _P, _SZ, _P]),
+    "kq_fp8_act_pack": (ctypes.c_int, [_I32, _P, _P, _I32, _P, _SZ, _P]),
+    "kq_fp8_act_unpack": (ctypes.c_int, [_I32, _P, _I32, _P, _P, _P, _I32, _P]),
+    "kq_fp8_gemm": (ctypes.c_int, [_F, _P, _P, _I32, _P, _I64, _I32, _P]),
+    "kq_fp8_gated_act": (ctypes.c_int, [_F, _P, _P, _I32, _P, _SZ, _P]),
+    "kq_fp8_linear": (ctypes.c_int, [_F, _P, _P, _I64, _I32, _P, _I64, _I32, _P, _SZ, _P]),
+    "kq_fp8_ffn": (ctypes.c_int, [_F, _P, _F, _P, _P, _I64, _P, _I64, _I32, _P, ctypes.c_float, _I32,
+                                  _P, _I64, _I32, _P, _SZ, _P]),
+    "kq_fp8_last_device_error": (ctypes.c_int, [_P, _P]),
 }
 for _name, (_res, _args) in _sigs.items():
     _f = getattr(lib, _name)
@@ -356,3 +391,264 @@ def debug_wait_timeout(layer: Layer, act, M: int, limit_us: int, stream=None) ->
     _need(act, __import__("torch").uint8, act_bytes(layer, M), "act")
     _check(lib.kq_debug_wait_timeout(layer.desc, _ptr(act), int(M), int(limit_us), _stream(stream)),
            "kq_debug_wait_timeout")
+
+
+# ---------------------------------------------------------------- 8-bit operators --------
+class Fp8Layer:
+    """One 8-bit linear layer (the C ``kq_fp8_desc``): E4M3 codes with a power-of-two scale for
+    each token and 128 features, and for each 128 x 128 piece of a weight. ``gated``: two
+    weights and ``activation(X Wgate) * (X Wup)``, ``activation`` ``"silu"`` or ``"gelu"`` (erf)."""
+
+    def __init__(self, K: int, N: int, gated: bool = False, activation: str = "silu"):
+        self.K, self.N, self.gated, self.activation = int(K), int(N), bool(gated), activation
+        self._desc = _Fp8Desc(K=self.K, N=self.N, gated=int(self.gated), activation=_ACTIVATION[activation])
+
+    @property
+    def desc(self):
+        return ctypes.byref(self._desc)
+
+
+def _rows(t, dtypes, rows: int | None, width: int, name: str) -> int:
+    """Checks a matrix whose rows may be a pitch apart and returns the pitch."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.dim() != 2 or t.shape[1] != width or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name} must be [{'M' if rows is None else rows}, {width}], got {list(t.shape)}")
+    if t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    # the pitch of a single row is of no consequence, and torch leaves it arbitrary
+    return int(t.stride(0)) if t.shape[0] > 1 else width
+
+
+class _Fp8Call:
+    """Runs a library call on the device of its tensors, which must all be on one device."""
+
+    def __init__(self, *tensors):
+        import torch
+        on = {t.device for t in tensors if t is not None}
+        if len(on) > 1:
+            raise ValueError(f"tensors are on different devices: {sorted(map(str, on))}")
+        self._guard = torch.cuda.device(on.pop())
+
+    def __enter__(self):
+        self._guard.__enter__()
+
+    def __exit__(self, *exc):
+        return self._guard.__exit__(*exc)
+
+
+def fp8_weights_bytes(layer: Fp8Layer) -> int:
+    return int(lib.kq_fp8_weights_bytes(layer.desc))
+
+
+def fp8_act_bytes(K: int, M: int) -> int:
+    return int(lib.kq_fp8_act_bytes(int(K), int(M)))
+
+
+def fp8_ffn_bytes(gated: Fp8Layer, down: Fp8Layer, M: int) -> int:
+    return int(lib.kq_fp8_ffn_bytes(gated.desc, down.desc, int(M)))
+
+
+def _fp8_pair(layer: Fp8Layer, up, name: str) -> None:
+    if (up is not None) != layer.gated:
+        raise ValueError(f"{name} goes with gated layers, and with those only")
+
+
+def _fp8_weights(layer: Fp8Layer, weights):
+    import torch
+    n = fp8_weights_bytes(layer)
+    if n == 0:
+        raise ValueError(f"unsupported 8-bit layer K={layer.K} N={layer.N}")
+    return _need(weights, torch.uint8, n, "weights")
+
+
+def _e4m3(t, numel: int, name: str):
+    import torch
+    if t is not None and t.dtype == torch.float8_e4m3fn:
+        t = t.view(torch.uint8)
+    return _need(t, torch.uint8, numel, name)
+
+
+def fp8_prepare_weights(layer: Fp8Layer, W, weights, W_up=None, stream=None) -> None:
+    """Quantize W (bf16 [K, N]; gated layers: W is the gate's and W_up the other) into weights."""
+    import torch
+    _fp8_pair(layer, W_up, "W_up")
+    _fp8_weights(layer, weights)
+    for t, name in ((W, "W"), (W_up, "W_up"))[:1 + layer.gated]:
+        _need(t, torch.bfloat16, layer.K * layer.N, name)
+    with _Fp8Call(W, W_up, weights):
+        _check(lib.kq_fp8_prepare_weights(layer.desc, _ptr(W), _ptr(W_up), _ptr(weights), _stream(stream)),
+               "kq_fp8_prepare_weights")
+
+
+def _fp8_parts(layer: Fp8Layer, codes, scales, up_codes, up_scales, optional: bool):
+    import torch
+    n, ns = layer.K * layer.N, -(-layer.N // 128) * -(-layer.K // 128)
+    parts = [codes, scales, up_codes, up_scales]
+    for i, (t, name) in enumerate(zip(parts, ("codes", "scales", "up_codes", "up_scales"))):
+        if t is None and (optional or (i > 1 and not layer.gated)):
+            continue
+        if i > 1 and not layer.gated:
+            raise ValueError(f"{name} goes with gated layers only")
+        parts[i] = _need(t, torch.uint8, ns, name) if i % 2 else _e4m3(t, n, name)
+    return parts
+
+
+def fp8_weights_pack(layer: Fp8Layer, codes, scales, weights, up_codes=None, up_scales=None, stream=None) -> None:
+    """Write weights from canonical parts: codes [N, K] (uint8 or float8_e4m3fn), scales uint8
+    [ceil(N / 128), ceil(K / 128)] (exponent + 127); gated layers take the up_ pair too."""
+    _fp8_weights(layer, weights)
+    parts = _fp8_parts(layer, codes, scales, up_codes, up_scales, optional=False)
+    with _Fp8Call(weights, *parts):
+        _check(lib.kq_fp8_weights_pack(layer.desc, *map(_ptr, parts), _ptr(weights), _stream(stream)),
+               "kq_fp8_weights_pack")
+
+
+def fp8_weights_unpack(layer: Fp8Layer, weights, codes=None, scales=None, up_codes=None, up_scales=None,
+                       stream=None) -> None:
+    _fp8_weights(layer, weights)
+    parts = _fp8_parts(layer, codes, scales, up_codes, up_scales, optional=True)
+    with _Fp8Call(weights, *parts):
+        _check(lib.kq_fp8_weights_unpack(layer.desc, _ptr(weights), *map(_ptr, parts), _stream(stream)),
+               "kq_fp8_weights_unpack")
+
+
+def _fp8_act(act, K: int, M: int, name: str = "act"):
+    import torch
+    return _need(act, torch.uint8, fp8_act_bytes(K, M), name)
+
+
+def fp8_quantize_act(X, act, stream=None) -> None:
+    """Quantize X (bf16 [M, K], rows may be a pitch apart) into an activation workspace."""
+    import torch
+    M, K = X.shape
+    ldx = _rows(X, (torch.bfloat16,), None, K, "X")
+    _fp8_act(act, K, M)
+    with _Fp8Call(X, act):
+        _check(lib.kq_fp8_quantize_act(K, _ptr(X), ldx, M, _ptr(act), act.numel(), _stream(stream)),
+               "kq_fp8_quantize_act")
+
+
+def _fp8_norm(gamma, residual, M: int, K: int):
+    """(residual pitch, residual dtype) after the checks."""
+    import torch
+    _need(gamma, torch.float32, K, "gamma")
+    if residual is None:
+        return 0, OUT_F32
+    ldr = _rows(residual, (torch.bfloat16, torch.float32), M, K, "residual")
+    return ldr, OUT_BF16 if residual.dtype == torch.bfloat16 else OUT_F32
+
+
+def fp8_rmsnorm_act(X, gamma, eps: float, act, residual=None, stream=None) -> None:
+    """Root-mean-square norm of X + residual times gamma, quantized into act; residual (bf16 or
+    fp32 [M, K]) is replaced by the sum."""
+    import torch
+    M, K = X.shape
+    ldx = _rows(X, (torch.bfloat16,), None, K, "X")
+    ldr, rdt = _fp8_norm(gamma, residual, M, K)
+    _fp8_act(act, K, M)
+    with _Fp8Call(X, gamma, residual, act):
+        _check(lib.kq_fp8_rmsnorm_act(K, _ptr(X), ldx, _ptr(residual), ldr, rdt, _ptr(gamma), float(eps), M,
+                                      _ptr(act), act.numel(), _stream(stream)), "kq_fp8_rmsnorm_act")
+
+
+def fp8_act_pack(K: int, codes, scales, M: int, act, stream=None) -> None:
+    import torch
+    codes = _e4m3(codes, M * K, "codes")
+    _need(scales, torch.uint8, M * -(-K // 128), "scales")
+    _fp8_act(act, K, M)
+    with _Fp8Call(codes, scales, act):
+        _check(lib.kq_fp8_act_pack(int(K), _ptr(codes), _ptr(scales), int(M), _ptr(act), act.numel(),
+                                   _stream(stream)), "kq_fp8_act_pack")
+
+
+def fp8_act_unpack(K: int, act, M: int, codes=None, scales=None, values=None, stream=None) -> None:
+    """Read an activation workspace: codes [M, K], scales uint8 [M, ceil(K / 128)], values (bf16
+    or fp32 [M, K]) = code * 2^(scale - 127); parts that are None are skipped."""
+    import torch
+    _fp8_act(act, K, M)
+    vdt = OUT_F32
+    if codes is not None:
+        codes = _e4m3(codes, M * K, "codes")
+    if scales is not None:
+        _need(scales, torch.uint8, M * -(-K // 128), "scales")
+    if values is not None:
+        vdt = OUT_BF16 if values.dtype == torch.bfloat16 else OUT_F32
+        _need(values, torch.bfloat16 if vdt == OUT_BF16 else torch.float32, M * K, "values")
+    with _Fp8Call(act, codes, scales, values):
+        _check(lib.kq_fp8_act_unpack(int(K), _ptr(act), int(M), _ptr(codes), _ptr(scales), _ptr(values), vdt,
+                                     _stream(stream)), "kq_fp8_act_unpack")
+
+
+def _fp8_y(Y, M: int, N: int, out_dtype: int) -> int:
+    import torch
+    return _rows(Y, (torch.bfloat16 if out_dtype == OUT_BF16 else torch.float32,), M, N, "Y")
+
+
+def fp8_gemm(layer: Fp8Layer, weights, act, M: int, Y, out_dtype: int = OUT_F32, stream=None) -> None:
+    """The layer on a filled activation workspace."""
+    _fp8_weights(layer, weights)
+    _fp8_act(act, layer.K, M)
+    ldy = _fp8_y(Y, M, layer.N, out_dtype)
+    with _Fp8Call(weights, act, Y):
+        _check(lib.kq_fp8_gemm(layer.desc, _ptr(weights), _ptr(act), int(M), _ptr(Y), ldy, int(out_dtype),
+                               _stream(stream)), "kq_fp8_gemm")
+
+
+def fp8_gated_act(layer: Fp8Layer, weights, act, M: int, out_act, stream=None) -> None:
+    """A gated layer whose output is quantized into out_act, the workspace of a following layer."""
+    _fp8_weights(layer, weights)
+    _fp8_act(act, layer.K, M)
+    _fp8_act(out_act, layer.N, M, "out_act")
+    with _Fp8Call(weights, act, out_act):
+        _check(lib.kq_fp8_gated_act(layer.desc, _ptr(weights), _ptr(act), int(M), _ptr(out_act),
+                                    out_act.numel(), _stream(stream)), "kq_fp8_gated_act")
+
+
+def fp8_linear(layer: Fp8Layer, weights, X, Y, act, out_dtype: int = OUT_F32, stream=None) -> None:
+    """Quantize X (bf16 [M, K]) into act and run the layer into Y [M, N]."""
+    import torch
+    M = X.shape[0]
+    _fp8_weights(layer, weights)
+    ldx = _rows(X, (torch.bfloat16,), None, layer.K, "X")
+    ldy = _fp8_y(Y, M, layer.N, out_dtype)
+    _fp8_act(act, layer.K, M)
+    with _Fp8Call(weights, X, Y, act):
+        _check(lib.kq_fp8_linear(layer.desc, _ptr(weights), _ptr(X), ldx, M, _ptr(Y), ldy, int(out_dtype),
+                                 _ptr(act), act.numel(), _stream(stream)), "kq_fp8_linear")
+
+
+def fp8_ffn(gated: Fp8Layer, gated_weights, down: Fp8Layer, down_weights, X, gamma, eps: float, Y, ws,
+            out_dtype: int = OUT_F32, residual=None, stream=None) -> None:
+    """A feed-forward block: rmsnorm of X + residual (gamma None: X as it is), the gated layer,
+    the down projection into Y. ws: uint8, fp8_ffn_bytes(gated, down, M)."""
+    import torch
+    M = X.shape[0]
+    _fp8_weights(gated, gated_weights)
+    _fp8_weights(down, down_weights)
+    need = fp8_ffn_bytes(gated, down, M)
+    if need == 0:
+        raise ValueError("fp8_ffn takes a gated layer and a plain one with K equal to its N, and M >= 1")
+    _need(ws, torch.uint8, need, "ws")
+    ldx = _rows(X, (torch.bfloat16,), None, gated.K, "X")
+    if gamma is None and residual is not None:
+        raise ValueError("residual needs gamma")
+    ldr, rdt = _fp8_norm(gamma, residual, M, gated.K) if gamma is not None else (0, OUT_F32)
+    ldy = _fp8_y(Y, M, down.N, out_dtype)
+    with _Fp8Call(gated_weights, down_weights, X, gamma, residual, Y, ws):
+        _check(lib.kq_fp8_ffn(gated.desc, _ptr(gated_weights), down.desc, _ptr(down_weights), _ptr(X), ldx,
+                              _ptr(residual), ldr, rdt, _ptr(gamma), float(eps), M, _ptr(Y), ldy,
+                              int(out_dtype), _ptr(ws), ws.numel(), _stream(stream)), "kq_fp8_ffn")
+
+
+def fp8_last_device_error(act, stream=None) -> int:
+    """0, or ERR_DEVICE_TIMEOUT if a bounded device wait ran out. Synchronises the stream and
+    clears the word."""
+    import torch
+    _need(act, torch.uint8, 256, "act")
+    with _Fp8Call(act):
+        return int(lib.kq_fp8_last_device_error(_ptr(act), _stream(stream)))

@@ -8,17 +8,16 @@
 #include <vector>
 
 #include "../../include/kq.h"
+#include "host.cuh"
 #include "kq_internal.cuh"
 #include "kq_pack.cuh"
 #include "kq_prepare.cuh"
 
 using namespace kq;
 
-namespace {
+namespace kq {
 
 // ------------------------------------------------------------------ device checks --
-struct DeviceInfo { bool ok = false; int sms = 0; int device = 0; };
-
 kq_status current_device(DeviceInfo* out) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return KQ_ERR_CUDA;
@@ -42,9 +41,9 @@ kq_status current_device(DeviceInfo* out) {
 }
 
 // -------------------------------------------------------------- tensor maps (TMA) --
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+static PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
-bool encode_fn() {
+static bool encode_fn() {
   static std::once_flag once;
   std::call_once(once, [] {
     cudaDriverEntryPointQueryResult q;
@@ -71,11 +70,15 @@ bool make_tmap(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// ---------------------------------------------------------------- validation --------
 // TMA tensor maps and bulk copies need 16-byte global addresses; every region the library
 // carves out of a caller buffer starts at a 1024-byte multiple from its base
 bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+}  // namespace kq
+
+namespace {
+
+// ---------------------------------------------------------------- validation --------
 constexpr int kRpbhMaxK = 32736;    // largest K % 32 == 0 with 2 K < 65536
 
 kq_status check_desc(const kq_layer_desc* d) {

@@ -1,0 +1,141 @@
+// The 8-bit operators: layouts of their buffers, encoding, kernel parameter blocks and
+// launcher prototypes.
+//
+// An 8-bit block is up to 128 consecutive features of one token (activations) or a
+// 128 x 128 piece of a weight: E4M3 codes and one scale 2^e (E8M0 byte e + 127). e is the
+// smallest exponent >= -127 for which no value exceeds 448 * 2^e, so nothing saturates;
+// byte 0 for a block of zeros. A block that holds an infinity or NaN gets byte 0xFF and NaN
+// codes: whatever is computed from it is NaN.
+//
+// Codes are row-major with the contraction dimension contiguous (what TMA loads as a K-major
+// MMA operand). Scale bytes are stored in the same 512-byte atoms as the MXFP4 scales
+// (layout.cuh: 128 rows x 4 blocks), but a block is 128 elements here: one atom serves four
+// 128-element k-tiles, k-tile t by byte t % 4.
+#pragma once
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "layout.cuh"
+#include "sm100.cuh"
+
+namespace kq {
+namespace fp8 {
+
+constexpr int kBlk = 128;                    // elements per scale along K; bytes per k-tile row
+constexpr int kNormMaxK = 32768;             // the norm keeps a row in registers
+
+__host__ __device__ constexpr int64_t katoms(int64_t K) { return cdiv(K, 4 * kBlk); }
+
+struct WLayout {
+  size_t codes[2] = {0, 0};                  // uint8 [N, K], gate (or the only one) and up
+  size_t sf[2] = {0, 0};                     // scale atoms, rows padded to 128
+  size_t total = 0;
+  __host__ __device__ static WLayout make(int64_t K, int64_t N, bool gated) {
+    WLayout L;
+    size_t o = 0;
+    for (int i = 0; i < (gated ? 2 : 1); ++i) {
+      L.codes[i] = o; o = align_up(o + static_cast<size_t>(N) * K, kAlign);
+      L.sf[i] = o;    o = align_up(o + static_cast<size_t>(cdiv(N, 128)) * katoms(K) * 512u, kAlign);
+    }
+    L.total = o;
+    return L;
+  }
+};
+
+struct ALayout {
+  size_t err = 0;                            // uint32 device error word
+  size_t codes = 0;                          // uint8 [M, K]
+  size_t sf = 0;                             // scale atoms, rows padded to 128
+  size_t total = 0;
+  __host__ __device__ static ALayout make(int64_t M, int64_t K) {
+    ALayout L;
+    size_t o = kHdrBytes;
+    L.codes = o = align_up(o, kAlign);
+    o = align_up(o + static_cast<size_t>(M) * K, kAlign);
+    L.sf = o;
+    L.total = align_up(o + static_cast<size_t>(cdiv(M, 128)) * katoms(K) * 512u, kAlign);
+    return L;
+  }
+};
+
+// ------------------------------------------------------------------------- encoding -----
+// Scale byte of a block whose largest magnitude has the bits `amax` (sign cleared). 448 is
+// 1.75 * 2^8: with amax = m 2^p, 1 <= m < 2, the exponent is p - 8, or p - 7 when m > 1.75,
+// read off the bits: adding 2^21 - 1 carries into the exponent exactly when the mantissa field
+// exceeds that of 1.75.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
+  if (amax >= 0x7F800000u) return 0xFFu;
+  const int32_t p = static_cast<int32_t>((amax + 0x1FFFFFu) >> 23) - 8;   // biased: e + 127
+  return static_cast<uint32_t>(p < 0 ? 0 : p);
+}
+// 2^-e of a scale byte e + 127 <= 247 as fp32 (exact: 2^-120 .. 2^127); the quotient of a
+// value by its scale is then exact or, below E4M3's smallest step, rounded far under it.
+__device__ __forceinline__ float inv_scale(uint32_t byte) {
+  return byte == 0xFFu ? __uint_as_float(0x7FC00000u) : __uint_as_float((254u - byte) << 23);
+}
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+  return byte == 0xFFu ? __uint_as_float(0x7FC00000u)
+                       : (byte == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(byte << 23));
+}
+// Two values -> two E4M3 codes (round to nearest even; NaN -> 0x7F), lo in the low byte.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
+}
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// --------------------------------------------------------------------- parameter blocks --
+struct NormParams {
+  const void* x;              // bf16 [M, ldx]
+  int64_t ldx;
+  void* residual;             // bf16 or fp32 [M, ldr], read and rewritten; null: none
+  int64_t ldr;
+  const float* gamma;         // [K]
+  double eps;
+  int M, K;
+  int64_t katoms;
+  uint8_t* codes;
+  uint8_t* sf;
+  uint32_t* err;              // cleared
+};
+
+struct MmParams {
+  CUtensorMap tmap_w[2];      // weight codes [N, K] (gate / only, up), box 128 bytes x 128 rows
+  CUtensorMap tmap_x;         // activation codes [M, K], box 128 bytes x token tile
+  const uint8_t* sfw[2];      // weight scale atoms
+  const uint8_t* sfx;         // activation scale atoms
+  int M, N, K;
+  int64_t katoms;             // of K
+  int act;                    // gated: 0 SiLU, 1 GELU
+  int out;                    // 0 fp32, 1 bf16, 2 8-bit blocks
+  void* y;                    // [M, ldy] fp32 / bf16
+  int64_t ldy;
+  uint8_t* ocodes;            // 8-bit output: codes [M, N], scale atoms, its katoms and error
+  uint8_t* osf;               //   word (cleared)
+  int64_t okatoms;
+  uint32_t* oerr;
+  int dependent;              // launched as a programmatic dependent of the kernel that writes
+                              //   the activations, whose predecessors had ended
+  uint32_t* err;
+};
+
+cudaError_t launch_rows(const NormParams& p, bool norm, int res_kind, cudaStream_t st);
+cudaError_t launch_weight_quant(const void* W, int K, int N, uint8_t* codes, uint8_t* sf, cudaStream_t st);
+cudaError_t launch_weight_scales(uint8_t* canonical, int K, int N, uint8_t* sf, bool pack, cudaStream_t st);
+cudaError_t launch_act_scales(uint8_t* canonical, int K, int M, uint8_t* sf, bool pack, cudaStream_t st);
+// values: fp32 or bf16 [M, K]
+cudaError_t launch_act_values(const uint8_t* codes, const uint8_t* sf, int K, int M, void* values, bool bf16,
+                              cudaStream_t st);
+// token tile of the product's kernel for M tokens (the box height of MmParams::tmap_x)
+int mm_token_tile(int M);
+cudaError_t launch_mm(const MmParams& p, bool gated, cudaStream_t st);
+
+}  // namespace fp8
+}  // namespace kq
