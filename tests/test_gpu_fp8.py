@@ -242,7 +242,8 @@ def test_pitched_rows_and_untouched_neighbours(cuda_device):
 # --------------------------------------------------------------------------- products ----
 SHAPES = [(1, 32, 16), (1, 4096, 256), (3, 96, 48), (16, 512, 128), (17, 544, 144), (32, 1152, 272), (33, 128, 400),
           (64, 640, 128), (65, 2080, 256), (127, 160, 272), (128, 384, 128), (129, 1024, 144), (200, 12288, 160),
-          (257, 1152, 528), (300, 96, 1040), (520, 736, 784), (1, 12288, 1040), (5, 8192, 640)]
+          (257, 1152, 528), (300, 96, 1040), (520, 736, 784), (1, 12288, 1040), (5, 8192, 640),
+          (2100, 160, 2320), (1300, 640, 4112)]         # several tiles for each CTA pair
 
 
 @pytest.mark.parametrize("out", ["f32", "bf16"])
@@ -273,7 +274,8 @@ def gated_bound(z, u, zerr, uerr, kind):
 
 @pytest.mark.parametrize("kind", ["silu", "gelu"])
 @pytest.mark.parametrize("M,K,N", [(1, 32, 16), (2, 4096, 128), (16, 160, 144), (20, 512, 272), (64, 1152, 256),
-                                   (65, 96, 400), (130, 2080, 272), (300, 640, 528), (1, 8192, 640)])
+                                   (65, 96, 400), (130, 2080, 272), (300, 640, 528), (1, 8192, 640), (1100, 160, 2080),
+                                   (700, 544, 4016)])
 def test_gated(cuda_device, M, K, N, kind):
     import torch
     import w4a4_post_quantization_token_b200 as kq

@@ -9,6 +9,7 @@ shared library is missing or cannot be loaded, importing this package raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -402,6 +403,7 @@ class Fp8Layer:
     def __init__(self, K: int, N: int, gated: bool = False, activation: str = "silu"):
         self.K, self.N, self.gated, self.activation = int(K), int(N), bool(gated), activation
         self._desc = _Fp8Desc(K=self.K, N=self.N, gated=int(self.gated), activation=_ACTIVATION[activation])
+        self._weights_bytes = fp8_weights_bytes(self)
 
     @property
     def desc(self):
@@ -424,27 +426,37 @@ def _rows(t, dtypes, rows: int | None, width: int, name: str) -> int:
     return int(t.stride(0)) if t.shape[0] > 1 else width
 
 
-class _Fp8Call:
-    """Runs a library call on the device of its tensors, which must all be on one device."""
-
-    def __init__(self, *tensors):
-        import torch
-        on = {t.device for t in tensors if t is not None}
-        if len(on) > 1:
-            raise ValueError(f"tensors are on different devices: {sorted(map(str, on))}")
-        self._guard = torch.cuda.device(on.pop())
-
-    def __enter__(self):
-        self._guard.__enter__()
-
-    def __exit__(self, *exc):
-        return self._guard.__exit__(*exc)
+def _fp8_run(fn, where: str, stream, tensors, *args) -> None:
+    """Calls fn(*args, stream) on the device of `tensors`, which must all be on one device, and
+    on `stream` or that device's current stream."""
+    import torch
+    dev = -1
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            if dev >= 0 and d != dev:
+                raise ValueError(f"{where}: tensors are on different devices")
+            dev = d
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device_index != dev:
+        raise ValueError(f"{where}: the stream is of another device than the tensors")
+    else:
+        raw = stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, raw)
+    if status != 0:
+        raise KQError(status, where)
 
 
 def fp8_weights_bytes(layer: Fp8Layer) -> int:
     return int(lib.kq_fp8_weights_bytes(layer.desc))
 
 
+@functools.lru_cache(maxsize=4096)
 def fp8_act_bytes(K: int, M: int) -> int:
     return int(lib.kq_fp8_act_bytes(int(K), int(M)))
 
@@ -460,10 +472,9 @@ def _fp8_pair(layer: Fp8Layer, up, name: str) -> None:
 
 def _fp8_weights(layer: Fp8Layer, weights):
     import torch
-    n = fp8_weights_bytes(layer)
-    if n == 0:
+    if layer._weights_bytes == 0:
         raise ValueError(f"unsupported 8-bit layer K={layer.K} N={layer.N}")
-    return _need(weights, torch.uint8, n, "weights")
+    return _need(weights, torch.uint8, layer._weights_bytes, "weights")
 
 
 def _e4m3(t, numel: int, name: str):
@@ -480,9 +491,8 @@ def fp8_prepare_weights(layer: Fp8Layer, W, weights, W_up=None, stream=None) -> 
     _fp8_weights(layer, weights)
     for t, name in ((W, "W"), (W_up, "W_up"))[:1 + layer.gated]:
         _need(t, torch.bfloat16, layer.K * layer.N, name)
-    with _Fp8Call(W, W_up, weights):
-        _check(lib.kq_fp8_prepare_weights(layer.desc, _ptr(W), _ptr(W_up), _ptr(weights), _stream(stream)),
-               "kq_fp8_prepare_weights")
+    _fp8_run(lib.kq_fp8_prepare_weights, "kq_fp8_prepare_weights", stream, (W, W_up, weights), layer.desc, _ptr(W),
+             _ptr(W_up), _ptr(weights))
 
 
 def _fp8_parts(layer: Fp8Layer, codes, scales, up_codes, up_scales, optional: bool):
@@ -503,18 +513,16 @@ def fp8_weights_pack(layer: Fp8Layer, codes, scales, weights, up_codes=None, up_
     [ceil(N / 128), ceil(K / 128)] (exponent + 127); gated layers take the up_ pair too."""
     _fp8_weights(layer, weights)
     parts = _fp8_parts(layer, codes, scales, up_codes, up_scales, optional=False)
-    with _Fp8Call(weights, *parts):
-        _check(lib.kq_fp8_weights_pack(layer.desc, *map(_ptr, parts), _ptr(weights), _stream(stream)),
-               "kq_fp8_weights_pack")
+    _fp8_run(lib.kq_fp8_weights_pack, "kq_fp8_weights_pack", stream, (weights, *parts), layer.desc, *map(_ptr,
+             parts), _ptr(weights))
 
 
 def fp8_weights_unpack(layer: Fp8Layer, weights, codes=None, scales=None, up_codes=None, up_scales=None,
-                       stream=None) -> None:
+                   stream=None) -> None:
     _fp8_weights(layer, weights)
     parts = _fp8_parts(layer, codes, scales, up_codes, up_scales, optional=True)
-    with _Fp8Call(weights, *parts):
-        _check(lib.kq_fp8_weights_unpack(layer.desc, _ptr(weights), *map(_ptr, parts), _stream(stream)),
-               "kq_fp8_weights_unpack")
+    _fp8_run(lib.kq_fp8_weights_unpack, "kq_fp8_weights_unpack", stream, (weights, *parts), layer.desc,
+             _ptr(weights), *map(_ptr, parts))
 
 
 def _fp8_act(act, K: int, M: int, name: str = "act"):
@@ -528,9 +536,8 @@ def fp8_quantize_act(X, act, stream=None) -> None:
     M, K = X.shape
     ldx = _rows(X, (torch.bfloat16,), None, K, "X")
     _fp8_act(act, K, M)
-    with _Fp8Call(X, act):
-        _check(lib.kq_fp8_quantize_act(K, _ptr(X), ldx, M, _ptr(act), act.numel(), _stream(stream)),
-               "kq_fp8_quantize_act")
+    _fp8_run(lib.kq_fp8_quantize_act, "kq_fp8_quantize_act", stream, (X, act), K, _ptr(X), ldx, M, _ptr(act),
+             act.numel())
 
 
 def _fp8_norm(gamma, residual, M: int, K: int):
@@ -551,9 +558,8 @@ def fp8_rmsnorm_act(X, gamma, eps: float, act, residual=None, stream=None) -> No
     ldx = _rows(X, (torch.bfloat16,), None, K, "X")
     ldr, rdt = _fp8_norm(gamma, residual, M, K)
     _fp8_act(act, K, M)
-    with _Fp8Call(X, gamma, residual, act):
-        _check(lib.kq_fp8_rmsnorm_act(K, _ptr(X), ldx, _ptr(residual), ldr, rdt, _ptr(gamma), float(eps), M,
-                                      _ptr(act), act.numel(), _stream(stream)), "kq_fp8_rmsnorm_act")
+    _fp8_run(lib.kq_fp8_rmsnorm_act, "kq_fp8_rmsnorm_act", stream, (X, gamma, residual, act), K, _ptr(X), ldx,
+             _ptr(residual), ldr, rdt, _ptr(gamma), float(eps), M, _ptr(act), act.numel())
 
 
 def fp8_act_pack(K: int, codes, scales, M: int, act, stream=None) -> None:
@@ -561,9 +567,8 @@ def fp8_act_pack(K: int, codes, scales, M: int, act, stream=None) -> None:
     codes = _e4m3(codes, M * K, "codes")
     _need(scales, torch.uint8, M * -(-K // 128), "scales")
     _fp8_act(act, K, M)
-    with _Fp8Call(codes, scales, act):
-        _check(lib.kq_fp8_act_pack(int(K), _ptr(codes), _ptr(scales), int(M), _ptr(act), act.numel(),
-                                   _stream(stream)), "kq_fp8_act_pack")
+    _fp8_run(lib.kq_fp8_act_pack, "kq_fp8_act_pack", stream, (codes, scales, act), int(K), _ptr(codes),
+             _ptr(scales), int(M), _ptr(act), act.numel())
 
 
 def fp8_act_unpack(K: int, act, M: int, codes=None, scales=None, values=None, stream=None) -> None:
@@ -579,9 +584,8 @@ def fp8_act_unpack(K: int, act, M: int, codes=None, scales=None, values=None, st
     if values is not None:
         vdt = OUT_BF16 if values.dtype == torch.bfloat16 else OUT_F32
         _need(values, torch.bfloat16 if vdt == OUT_BF16 else torch.float32, M * K, "values")
-    with _Fp8Call(act, codes, scales, values):
-        _check(lib.kq_fp8_act_unpack(int(K), _ptr(act), int(M), _ptr(codes), _ptr(scales), _ptr(values), vdt,
-                                     _stream(stream)), "kq_fp8_act_unpack")
+    _fp8_run(lib.kq_fp8_act_unpack, "kq_fp8_act_unpack", stream, (act, codes, scales, values), int(K), _ptr(act),
+             int(M), _ptr(codes), _ptr(scales), _ptr(values), vdt)
 
 
 def _fp8_y(Y, M: int, N: int, out_dtype: int) -> int:
@@ -594,9 +598,8 @@ def fp8_gemm(layer: Fp8Layer, weights, act, M: int, Y, out_dtype: int = OUT_F32,
     _fp8_weights(layer, weights)
     _fp8_act(act, layer.K, M)
     ldy = _fp8_y(Y, M, layer.N, out_dtype)
-    with _Fp8Call(weights, act, Y):
-        _check(lib.kq_fp8_gemm(layer.desc, _ptr(weights), _ptr(act), int(M), _ptr(Y), ldy, int(out_dtype),
-                               _stream(stream)), "kq_fp8_gemm")
+    _fp8_run(lib.kq_fp8_gemm, "kq_fp8_gemm", stream, (weights, act, Y), layer.desc, _ptr(weights), _ptr(act),
+             int(M), _ptr(Y), ldy, int(out_dtype))
 
 
 def fp8_gated_act(layer: Fp8Layer, weights, act, M: int, out_act, stream=None) -> None:
@@ -604,9 +607,8 @@ def fp8_gated_act(layer: Fp8Layer, weights, act, M: int, out_act, stream=None) -
     _fp8_weights(layer, weights)
     _fp8_act(act, layer.K, M)
     _fp8_act(out_act, layer.N, M, "out_act")
-    with _Fp8Call(weights, act, out_act):
-        _check(lib.kq_fp8_gated_act(layer.desc, _ptr(weights), _ptr(act), int(M), _ptr(out_act),
-                                    out_act.numel(), _stream(stream)), "kq_fp8_gated_act")
+    _fp8_run(lib.kq_fp8_gated_act, "kq_fp8_gated_act", stream, (weights, act, out_act), layer.desc, _ptr(weights),
+             _ptr(act), int(M), _ptr(out_act), out_act.numel())
 
 
 def fp8_linear(layer: Fp8Layer, weights, X, Y, act, out_dtype: int = OUT_F32, stream=None) -> None:
@@ -617,9 +619,8 @@ def fp8_linear(layer: Fp8Layer, weights, X, Y, act, out_dtype: int = OUT_F32, st
     ldx = _rows(X, (torch.bfloat16,), None, layer.K, "X")
     ldy = _fp8_y(Y, M, layer.N, out_dtype)
     _fp8_act(act, layer.K, M)
-    with _Fp8Call(weights, X, Y, act):
-        _check(lib.kq_fp8_linear(layer.desc, _ptr(weights), _ptr(X), ldx, M, _ptr(Y), ldy, int(out_dtype),
-                                 _ptr(act), act.numel(), _stream(stream)), "kq_fp8_linear")
+    _fp8_run(lib.kq_fp8_linear, "kq_fp8_linear", stream, (weights, X, Y, act), layer.desc, _ptr(weights), _ptr(X),
+             ldx, M, _ptr(Y), ldy, int(out_dtype), _ptr(act), act.numel())
 
 
 def fp8_ffn(gated: Fp8Layer, gated_weights, down: Fp8Layer, down_weights, X, gamma, eps: float, Y, ws,
@@ -639,10 +640,9 @@ def fp8_ffn(gated: Fp8Layer, gated_weights, down: Fp8Layer, down_weights, X, gam
         raise ValueError("residual needs gamma")
     ldr, rdt = _fp8_norm(gamma, residual, M, gated.K) if gamma is not None else (0, OUT_F32)
     ldy = _fp8_y(Y, M, down.N, out_dtype)
-    with _Fp8Call(gated_weights, down_weights, X, gamma, residual, Y, ws):
-        _check(lib.kq_fp8_ffn(gated.desc, _ptr(gated_weights), down.desc, _ptr(down_weights), _ptr(X), ldx,
-                              _ptr(residual), ldr, rdt, _ptr(gamma), float(eps), M, _ptr(Y), ldy,
-                              int(out_dtype), _ptr(ws), ws.numel(), _stream(stream)), "kq_fp8_ffn")
+    _fp8_run(lib.kq_fp8_ffn, "kq_fp8_ffn", stream, (gated_weights, down_weights, X, gamma, residual, Y, ws),
+             gated.desc, _ptr(gated_weights), down.desc, _ptr(down_weights), _ptr(X), ldx, _ptr(residual), ldr,
+             rdt, _ptr(gamma), float(eps), M, _ptr(Y), ldy, int(out_dtype), _ptr(ws), ws.numel())
 
 
 def fp8_last_device_error(act, stream=None) -> int:
@@ -650,5 +650,5 @@ def fp8_last_device_error(act, stream=None) -> int:
     clears the word."""
     import torch
     _need(act, torch.uint8, 256, "act")
-    with _Fp8Call(act):
+    with torch.cuda.device(act.device):
         return int(lib.kq_fp8_last_device_error(_ptr(act), _stream(stream)))

@@ -109,6 +109,9 @@ struct NormParams {
 struct MmParams {
   CUtensorMap tmap_w[2];      // weight codes [N, K] (gate / only, up), box 128 bytes x 128 rows
   CUtensorMap tmap_x;         // activation codes [M, K], box 128 bytes x token tile
+  CUtensorMap tmap_sfw[2];    // pairs: weight and activation scale atoms as [atoms, 512 bytes]
+  CUtensorMap tmap_sfx;
+  CUtensorMap tmap_y;         // pairs: the output (codes when 8-bit), box 64 bytes x 32 rows
   const uint8_t* sfw[2];      // weight scale atoms
   const uint8_t* sfx;         // activation scale atoms
   int M, N, K;
@@ -121,6 +124,7 @@ struct MmParams {
   uint8_t* osf;               //   word (cleared)
   int64_t okatoms;
   uint32_t* oerr;
+  int pairs;                  // 1: k_mm_pair, 0: k_mm_rows
   int dependent;              // launched as a programmatic dependent of the kernel that writes
                               //   the activations, whose predecessors had ended
   uint32_t* err;
@@ -133,9 +137,11 @@ cudaError_t launch_act_scales(uint8_t* canonical, int K, int M, uint8_t* sf, boo
 // values: fp32 or bf16 [M, K]
 cudaError_t launch_act_values(const uint8_t* codes, const uint8_t* sf, int K, int M, void* values, bool bf16,
                               cudaStream_t st);
+// whether k_mm_pair is taken (else k_mm_rows)
+bool mm_by_pairs(int M, int N, int K, bool gated, int sms);
 // token tile of the product's kernel for M tokens (the box height of MmParams::tmap_x)
 int mm_token_tile(int M);
-cudaError_t launch_mm(const MmParams& p, bool gated, cudaStream_t st);
+cudaError_t launch_mm(const MmParams& p, bool gated, int sms, cudaStream_t st);
 
 }  // namespace fp8
 }  // namespace kq
