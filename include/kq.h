@@ -424,7 +424,9 @@ kq_status kq_fp8_gemm(const kq_fp8_desc *desc, const void *weights, void *act, i
 kq_status kq_fp8_gated_act(const kq_fp8_desc *desc, const void *weights, void *act, int32_t M,
                            void *out_act, size_t out_act_bytes, kq_stream_t stream);
 
-/* kq_fp8_quantize_act, then kq_fp8_gemm. */
+/* The layer on bf16 activations: the result of kq_fp8_quantize_act followed by kq_fp8_gemm. `act`
+ * is scratch; whether the encoded activations are in it afterwards is not specified (for few
+ * tokens the product's kernel encodes them on the way in). */
 kq_status kq_fp8_linear(const kq_fp8_desc *desc, const void *weights, const void *X_bf16, int64_t ldx,
                         int32_t M, void *Y, int64_t ldy, int32_t out_dtype, void *act,
                         size_t act_bytes, kq_stream_t stream);

@@ -243,7 +243,8 @@ def test_pitched_rows_and_untouched_neighbours(cuda_device):
 SHAPES = [(1, 32, 16), (1, 4096, 256), (3, 96, 48), (16, 512, 128), (17, 544, 144), (32, 1152, 272), (33, 128, 400),
           (64, 640, 128), (65, 2080, 256), (127, 160, 272), (128, 384, 128), (129, 1024, 144), (200, 12288, 160),
           (257, 1152, 528), (300, 96, 1040), (520, 736, 784), (1, 12288, 1040), (5, 8192, 640),
-          (2100, 160, 2320), (1300, 640, 4112)]         # several tiles for each CTA pair
+          (2100, 160, 2320), (1300, 640, 4112),         # several tiles for each CTA pair
+          (20, 2304, 9488), (31, 12288, 144), (16, 160, 272)]
 
 
 @pytest.mark.parametrize("out", ["f32", "bf16"])
@@ -297,6 +298,7 @@ def test_gated(cuda_device, M, K, N, kind):
     # 8-bit output: half a step of the E4M3 grid under the block's own scale, which holds the
     # block's largest value and is no larger than it needs to be
     h = buf(kq.fp8_act_bytes(N, M))
+    kq.fp8_quantize_act(X.cuda(), act)
     kq.fp8_gated_act(L, w, act, M, h)
     c, s = unpack(kq, h, M, N)
     scale = np.repeat(np.ldexp(1.0, s.astype(int) - 127), 128, 1)[:, :N]
@@ -432,6 +434,8 @@ def test_repacked_weights_are_read_at_once(cuda_device):
     L = kq.Fp8Layer(K, N)
     X = tokens(M, K, 2).cuda()
     act = buf(kq.fp8_act_bytes(K, M))
+    kq.fp8_quantize_act(X, act)
+    filled = act.clone()
     parts = [[_t(a) for a in fp8.encode_weight(_np(weight(K, N, s)))] for s in (1, 2)]
     want = []
     for p in parts:
@@ -446,7 +450,7 @@ def test_repacked_weights_are_read_at_once(cuda_device):
         for p, y in zip(parts, want):
             Y = torch.empty(M, N, device="cuda")
             kq.fp8_weights_pack(L, *p, w)
-            kq.fp8_gemm(L, w, act, M, Y)
+            kq.fp8_gemm(L, w, filled, M, Y)
             Y2 = torch.empty(M, N, device="cuda")
             kq.fp8_weights_pack(L, *p, w)
             kq.fp8_linear(L, w, X, Y2, act)

@@ -418,12 +418,14 @@ def _rows(t, dtypes, rows: int | None, width: int, name: str) -> int:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if t.dim() != 2 or t.shape[1] != width or (rows is not None and t.shape[0] != rows):
-        raise ValueError(f"{name} must be [{'M' if rows is None else rows}, {width}], got {list(t.shape)}")
-    if t.stride(1) != 1:
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != width or (rows is not None and shape[0] != rows):
+        raise ValueError(f"{name} must be [{'M' if rows is None else rows}, {width}], got {list(shape)}")
+    pitch, step = t.stride()
+    if step != 1:
         raise ValueError(f"{name} must have contiguous rows")
     # the pitch of a single row is of no consequence, and torch leaves it arbitrary
-    return int(t.stride(0)) if t.shape[0] > 1 else width
+    return pitch if shape[0] > 1 else width
 
 
 def _fp8_run(fn, where: str, stream, tensors, *args) -> None:

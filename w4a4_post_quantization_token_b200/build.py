@@ -17,7 +17,7 @@ ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 LIB_PATH = os.path.join(PKG_DIR, "libkq.so")
 SOURCES = ["api.cu", "quantize.cu", "gemm.cu", "prepare.cu", "pack.cu", "noalloc.cu",
-           "fp8_api.cu", "fp8_quant.cu", "fp8_mm.cu"]
+           "fp8_api.cu", "fp8_quant.cu", "fp8_rows.cu", "fp8_pair.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

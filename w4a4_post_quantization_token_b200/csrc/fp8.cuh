@@ -91,6 +91,32 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 }
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
+// 8 bf16 values of 16 bytes.
+__device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+// The scale byte of a block that 16 neighbouring lanes hold, 8 values each.
+__device__ __forceinline__ uint32_t block_byte(const float (&v)[8]) {
+  uint32_t a = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a = max(a, abs_bits(v[i]));
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+  return scale_byte(a);
+}
+
+// SiLU g / (1 + e^-g); GELU in its erf form, g erfc(-g / sqrt 2) / 2
+template <int ACT>
+__device__ __forceinline__ float gate_act(float g) {
+  if (ACT == 0) return __fdividef(g, 1.f + __expf(-g));
+  return 0.5f * g * erfcf(-0.70710678118654752f * g);
+}
+
 // --------------------------------------------------------------------- parameter blocks --
 struct NormParams {
   const void* x;              // bf16 [M, ldx]
@@ -107,13 +133,14 @@ struct NormParams {
 };
 
 struct MmParams {
-  CUtensorMap tmap_w[2];      // weight codes [N, K] (gate / only, up), box 128 bytes x 128 rows
-  CUtensorMap tmap_x;         // activation codes [M, K], box 128 bytes x token tile
+  CUtensorMap tmap_w[2];      // weight codes [N, K] (gate / only, up), box 128 bytes x (64, 96 or 128) rows
+  CUtensorMap tmap_x;         // activation codes [M, K], box 128 bytes x token tile (128 for k_mm_pair)
   CUtensorMap tmap_sfw[2];    // pairs: weight and activation scale atoms as [atoms, 512 bytes]
   CUtensorMap tmap_sfx;
-  CUtensorMap tmap_y;         // pairs: the output (codes when 8-bit), box 64 bytes x 32 rows
   const uint8_t* sfw[2];      // weight scale atoms
   const uint8_t* sfx;         // activation scale atoms
+  const void* xb;             // encoded on the way in: bf16 [M, ldx] instead of tmap_x and sfx
+  int64_t ldx;
   int M, N, K;
   int64_t katoms;             // of K
   int act;                    // gated: 0 SiLU, 1 GELU
@@ -124,7 +151,7 @@ struct MmParams {
   uint8_t* osf;               //   word (cleared)
   int64_t okatoms;
   uint32_t* oerr;
-  int pairs;                  // 1: k_mm_pair, 0: k_mm_rows
+  int pairs;                  // weight rows of k_mm_pair's tile, 0: k_rows_mm
   int dependent;              // launched as a programmatic dependent of the kernel that writes
                               //   the activations, whose predecessors had ended
   uint32_t* err;
@@ -137,11 +164,18 @@ cudaError_t launch_act_scales(uint8_t* canonical, int K, int M, uint8_t* sf, boo
 // values: fp32 or bf16 [M, K]
 cudaError_t launch_act_values(const uint8_t* codes, const uint8_t* sf, int K, int M, void* values, bool bf16,
                               cudaStream_t st);
-// whether k_mm_pair is taken (else k_mm_rows)
-bool mm_by_pairs(int M, int N, int K, bool gated, int sms);
-// token tile of the product's kernel for M tokens (the box height of MmParams::tmap_x)
-int mm_token_tile(int M);
-cudaError_t launch_mm(const MmParams& p, bool gated, int sms, cudaStream_t st);
+struct Device { int sms, device; };
+
+constexpr int kRowsMaxM = 64;                // tokens that k_rows_mm takes; more go to k_mm_pair
+// Weight rows of k_mm_pair's tile, 0 where k_rows_mm is taken; the box height of MmParams::tmap_w
+// is half of them (128 for k_rows_mm).
+int pair_cols(int M, int N, int K, bool gated, int sms);
+cudaError_t launch_pair(const MmParams& p, bool gated, int sms, cudaStream_t st);
+// token tile of k_rows_mm (the box height of MmParams::tmap_x; 128 for k_mm_pair)
+int rows_token_tile(int M);
+cudaError_t launch_rows_mm(const MmParams& p, bool gated, const Device& d, cudaStream_t st);
+// k_rows_mm on bf16 activations (p.xb), which it encodes itself; false where it does not take them
+bool try_rows_fused(const MmParams& p, bool gated, const Device& d, cudaStream_t st, cudaError_t* e);
 
 }  // namespace fp8
 }  // namespace kq

@@ -78,31 +78,30 @@ kq_status run_rows(int32_t K, const void* X, int64_t ldx, const Norm* n, int32_t
 }
 
 // Y (out 0 / 1) or the 8-bit workspace `oact` (out 2) from the activations in `act`.
-kq_status run_mm(const kq_fp8_desc* d, const void* weights, const uint8_t* act, int32_t M, int out, void* Y,
-                 int64_t ldy, uint8_t* oact, uint32_t* err, bool dependent, int sms, cudaStream_t st) {
+kq_status run_mm(const kq_fp8_desc* d, const void* weights, uint8_t* act, int32_t M, int out, void* Y,
+                 int64_t ldy, uint8_t* oact, uint32_t* err, bool dependent, const DeviceInfo& di, cudaStream_t st,
+                 const void* xb = nullptr, int64_t ldx = 0) {
   const fp8::WLayout W = wlayout(d);
   const fp8::ALayout A = fp8::ALayout::make(M, d->K);
   const uint8_t* w = static_cast<const uint8_t*>(weights);
   fp8::MmParams p;
   std::memset(&p, 0, sizeof(p));
   const uint64_t K = static_cast<uint64_t>(d->K);
+  const fp8::Device dev = {di.sms, di.device};
+  p.pairs = fp8::pair_cols(M, d->N, d->K, d->gated != 0, di.sms);
+  const uint32_t wrows = p.pairs ? static_cast<uint32_t>(p.pairs / 2) : 128;
   for (int i = 0; i < 1 + d->gated; ++i) {
     if (!make_tmap(&p.tmap_w[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, w + W.codes[i], K, static_cast<uint64_t>(d->N), K,
-                   128, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+                   128, wrows, CU_TENSOR_MAP_SWIZZLE_128B))
       return KQ_ERR_CUDA;
     p.sfw[i] = w + W.sf[i];
   }
-  if (!make_tmap(&p.tmap_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, act + A.codes, K, static_cast<uint64_t>(M), K, 128,
-                 static_cast<uint32_t>(fp8::mm_token_tile(M)), CU_TENSOR_MAP_SWIZZLE_128B))
-    return KQ_ERR_CUDA;
-  p.sfx = act + A.sf;
   p.M = M; p.N = d->N; p.K = d->K;
   p.katoms = fp8::katoms(d->K);
   p.act = d->activation;
   p.out = out;
   p.y = Y;
   p.ldy = ldy;
-  p.dependent = dependent ? 1 : 0;
   p.err = err;
   if (out == 2) {
     const fp8::ALayout O = fp8::ALayout::make(M, d->N);
@@ -111,26 +110,30 @@ kq_status run_mm(const kq_fp8_desc* d, const void* weights, const uint8_t* act, 
     p.okatoms = fp8::katoms(d->N);
     p.oerr = reinterpret_cast<uint32_t*>(oact + O.err);
   }
-  p.pairs = fp8::mm_by_pairs(M, d->N, d->K, d->gated != 0, sms) ? 1 : 0;
-  if (p.pairs) {
-    auto atoms = [&](CUtensorMap* m, const uint8_t* sf, int64_t rows) {
-      return make_tmap(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, sf, 128, static_cast<uint64_t>(cdiv(rows, 128) * p.katoms),
-                       512, 128, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
-    };
-    if (!atoms(&p.tmap_sfx, p.sfx, M)) return KQ_ERR_CUDA;
-    for (int i = 0; i < 1 + d->gated; ++i)
-      if (!atoms(&p.tmap_sfw[i], p.sfw[i], d->N)) return KQ_ERR_CUDA;
-    const uint64_t N = static_cast<uint64_t>(d->N), rows = static_cast<uint64_t>(M);
-    const bool ok =
-        out == 0 ? make_tmap(&p.tmap_y, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, Y, N, rows, static_cast<uint64_t>(ldy) * 4, 16,
-                             32, CU_TENSOR_MAP_SWIZZLE_64B)
-        : out == 1 ? make_tmap(&p.tmap_y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, Y, N, rows, static_cast<uint64_t>(ldy) * 2,
-                               32, 32, CU_TENSOR_MAP_SWIZZLE_64B)
-                   : make_tmap(&p.tmap_y, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.ocodes, N, rows, N, 64, 32,
-                               CU_TENSOR_MAP_SWIZZLE_64B);
-    if (!ok) return KQ_ERR_CUDA;
+  if (xb) {
+    // bf16 activations: few tokens are encoded by the product's own kernel
+    p.xb = xb;
+    p.ldx = ldx;
+    cudaError_t e = cudaSuccess;
+    if (!p.pairs && fp8::try_rows_fused(p, d->gated != 0, dev, st, &e)) return e == cudaSuccess ? KQ_OK : KQ_ERR_CUDA;
+    const kq_status s = run_rows(d->K, xb, ldx, nullptr, M, act, st);
+    if (s != KQ_OK) return s;
+    dependent = true;
   }
-  return fp8::launch_mm(p, d->gated != 0, sms, st) == cudaSuccess ? KQ_OK : KQ_ERR_CUDA;
+  p.dependent = dependent ? 1 : 0;
+  if (!make_tmap(&p.tmap_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, act + A.codes, K, static_cast<uint64_t>(M), K, 128,
+                 static_cast<uint32_t>(p.pairs ? 128 : fp8::rows_token_tile(M)), CU_TENSOR_MAP_SWIZZLE_128B))
+    return KQ_ERR_CUDA;
+  p.sfx = act + A.sf;
+  if (!p.pairs) return fp8::launch_rows_mm(p, d->gated != 0, dev, st) == cudaSuccess ? KQ_OK : KQ_ERR_CUDA;
+  auto atoms = [&](CUtensorMap* m, const uint8_t* sf, int64_t rows) {
+    return make_tmap(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, sf, 128, static_cast<uint64_t>(cdiv(rows, 128) * p.katoms), 512,
+                     128, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
+  };
+  if (!atoms(&p.tmap_sfx, p.sfx, M)) return KQ_ERR_CUDA;
+  for (int i = 0; i < 1 + d->gated; ++i)
+    if (!atoms(&p.tmap_sfw[i], p.sfw[i], d->N)) return KQ_ERR_CUDA;
+  return fp8::launch_pair(p, d->gated != 0, di.sms, st) == cudaSuccess ? KQ_OK : KQ_ERR_CUDA;
 }
 
 uint32_t* err_word(void* act) { return reinterpret_cast<uint32_t*>(act); }
@@ -286,7 +289,7 @@ kq_status kq_fp8_gemm(const kq_fp8_desc* desc, const void* weights, void* act, i
   DeviceInfo di;
   if ((s = current_device(&di)) != KQ_OK) return s;
   return run_mm(desc, weights, static_cast<uint8_t*>(act), M, out_dtype == KQ_OUT_BF16 ? 1 : 0, Y, ldy, nullptr,
-                err_word(act), false, di.sms, reinterpret_cast<cudaStream_t>(stream));
+                err_word(act), false, di, reinterpret_cast<cudaStream_t>(stream));
 }
 
 kq_status kq_fp8_gated_act(const kq_fp8_desc* desc, const void* weights, void* act, int32_t M, void* out_act,
@@ -300,7 +303,7 @@ kq_status kq_fp8_gated_act(const kq_fp8_desc* desc, const void* weights, void* a
   DeviceInfo di;
   if ((s = current_device(&di)) != KQ_OK) return s;
   return run_mm(desc, weights, static_cast<uint8_t*>(act), M, 2, nullptr, 0, static_cast<uint8_t*>(out_act),
-                err_word(act), false, di.sms, reinterpret_cast<cudaStream_t>(stream));
+                err_word(act), false, di, reinterpret_cast<cudaStream_t>(stream));
 }
 
 kq_status kq_fp8_linear(const kq_fp8_desc* desc, const void* weights, const void* X_bf16, int64_t ldx, int32_t M,
@@ -316,8 +319,8 @@ kq_status kq_fp8_linear(const kq_fp8_desc* desc, const void* weights, const void
   if ((s = current_device(&di)) != KQ_OK) return s;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* a = static_cast<uint8_t*>(act);
-  if ((s = run_rows(desc->K, X_bf16, ldx, nullptr, M, a, st)) != KQ_OK) return s;
-  return run_mm(desc, weights, a, M, out_dtype == KQ_OUT_BF16 ? 1 : 0, Y, ldy, nullptr, err_word(a), true, di.sms, st);
+  return run_mm(desc, weights, a, M, out_dtype == KQ_OUT_BF16 ? 1 : 0, Y, ldy, nullptr, err_word(a), false, di, st,
+                X_bf16, ldx);
 }
 
 kq_status kq_fp8_ffn(const kq_fp8_desc* gated, const void* gated_weights, const kq_fp8_desc* down,
@@ -341,8 +344,8 @@ kq_status kq_fp8_ffn(const kq_fp8_desc* gated, const void* gated_weights, const 
   uint8_t* a = static_cast<uint8_t*>(ws);
   uint8_t* h = a + fp8::ALayout::make(M, gated->K).total;
   if ((s = run_rows(gated->K, X_bf16, ldx, gamma ? &n : nullptr, M, a, st)) != KQ_OK) return s;
-  if ((s = run_mm(gated, gated_weights, a, M, 2, nullptr, 0, h, err_word(a), true, di.sms, st)) != KQ_OK) return s;
-  return run_mm(down, down_weights, h, M, out_dtype == KQ_OUT_BF16 ? 1 : 0, Y, ldy, nullptr, err_word(a), true, di.sms, st);
+  if ((s = run_mm(gated, gated_weights, a, M, 2, nullptr, 0, h, err_word(a), true, di, st)) != KQ_OK) return s;
+  return run_mm(down, down_weights, h, M, out_dtype == KQ_OUT_BF16 ? 1 : 0, Y, ldy, nullptr, err_word(a), true, di, st);
 }
 
 kq_status kq_fp8_last_device_error(void* act, kq_stream_t stream) {

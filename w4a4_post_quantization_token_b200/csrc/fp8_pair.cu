@@ -1,0 +1,420 @@
+// Block-scaled 8-bit matrix product on the 5th-generation tensor cores, for many tokens
+// (fp8_rows.cu has the product for few, and the formulas).
+//
+// k_mm_pair: 256 tokens x BN weight rows per pair of CTAs (gated: BN = 256, 128 of the gate and the
+// same 128 of up, so that both halves of an output meet in one thread). The two CTAs of a cluster
+// run one MMA of M = 256 (cta_group::2): each stages its own 128 tokens and half of the weight
+// rows, 32 KB per 128-element k-tile of 256 x 256 instead of the 48 KB that a 128 x 256 tile of
+// one CTA would need. The MMAs of such a k-tile take 512 cycles, so a CTA pulls 64 bytes a cycle,
+// the most that an SM gets from L2. Persistent, one pair per two SMs. Warp roles:
+//   warps 0, 10  TMA producers in each CTA, of the tokens and of the weights; all loads of a
+//              stage, the peer's too, complete on the first CTA's barrier.
+//   warp 1     TMEM allocator; in the first CTA the MMA issuer for both.
+//   warps 2-9  epilogue: thread = token, two warps share a TMEM lane quadrant and take half of
+//              the columns each and write them through staging buffers in whole pieces of rows.
+// TMEM holds two accumulators and the scales behind them. Up to BN = 192 they are apart, and one
+// tile's epilogue runs beside the next tile's MMAs. Two of 256 columns overlap in 64 (0 .. 255
+// and 192 .. 447): the epilogue reads the shared 64 columns first, and the next tile's MMAs start
+// when those are out, some 1800 cycles after the last MMA.
+#include <cuda_bf16.h>
+
+#include "fp8.cuh"
+#include "sm100_fp8.cuh"
+
+namespace kq {
+namespace fp8 {
+
+namespace {
+
+template <int BN>
+struct Pair {
+  static constexpr bool kShared = BN == 256;
+  static constexpr int kStages = BN == 256 ? 5 : 6;
+  static constexpr uint32_t kATile = 128 * 128;
+  static constexpr uint32_t kBTile = BN / 2 * 128;
+  static constexpr uint32_t kStageBytes = kATile + kBTile;           // tokens, weight rows
+  static constexpr int kWAtoms = BN == 128 ? 1 : 2;                  // scale atoms of the weight rows
+  static constexpr uint32_t kSfBytes = (1 + kWAtoms) * 512;
+  static constexpr uint32_t kStgBytes = 4096;                        // a warp's 32 rows x 128 bytes
+  static constexpr uint32_t kRingOff = 1024;
+  static constexpr uint32_t kStgOff = kRingOff + kStages * kStageBytes;
+  static constexpr uint32_t kSfOff = kStgOff + 8 * kStgBytes;
+  static constexpr uint32_t kTopOff = kSfOff + kStages * kSfBytes;   // uint32 [2 halves][128 rows]
+  static constexpr uint32_t kSmem = 1024 + kTopOff + 1024;
+  static constexpr uint32_t kAccStride = kShared ? 192 : BN;
+  // Scale sets of 12 columns (tokens 4, weight rows 8), used in turn by the atoms. A set comes
+  // round after kSets >= kStages atoms, so after kStages k-tiles at least: its last MMAs have
+  // freed the stage that the new atom landed in.
+  static constexpr uint32_t kSfCol = kAccStride + BN, kSfSet = 12;
+  static constexpr int kSets = kStages;
+  static constexpr int kThreads = 352;
+  static_assert(kSmem <= 232448 && kSfCol + kSets * kSfSet <= 512, "shared memory, TMEM");
+  static_assert(kStageBytes % 1024 == 0, "swizzle atoms");
+};
+
+// Tile order: groups of 8 row tiles, row tile fastest, so that the pairs at work share a few
+// row tiles and a few column tiles in L2.
+__device__ __forceinline__ void pair_tile(int tile, int MT, int NT, int& mt, int& nt) {
+  const int per = 8 * NT, g = tile / per, r = tile - g * per;
+  const int gm = min(8, MT - g * 8);
+  mt = g * 8 + r % gm;
+  nt = r / gm;
+}
+
+// Writes W words (64 or 128 bytes) of each of a warp's 32 rows: through
+// a swizzled staging buffer, so that a store instruction covers whole 64- or 128-byte pieces of
+// rows. (TMA stores of the same boxes compete with the operand loads for the TMA unit: the fc1
+// product of 4096 x 1152 -> 4608 took 33 us with them.) `col` and `pitch` in bytes; `cols` bytes
+// of the row exist from col on, `rows` rows from this warp's first.
+template <int W>
+__device__ __forceinline__ void put_rows(const uint32_t (&w)[W], uint8_t* stg, uint8_t* out, int64_t pitch, int cols,
+                                         int rows, int lane) {
+  constexpr int kChunks = W / 4;                                     // 16-byte chunks per row: 4 or 8
+  constexpr int kStep = 32 / kChunks;                                // rows per store instruction
+  __syncwarp();                                                      // the last call's reads are done
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+    const int sw = kChunks == 8 ? c ^ (lane & 7) : c ^ ((lane >> 1) & 3);
+    *reinterpret_cast<uint4*>(stg + lane * (16 * kChunks) + 16 * sw) =
+        make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+  }
+  __syncwarp();
+  const int c = lane % kChunks;
+  if (16 * c >= cols) return;
+  uint4 v[kChunks];
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    const int r = i * kStep + lane / kChunks;
+    const int sw = kChunks == 8 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
+    v[i] = *reinterpret_cast<const uint4*>(stg + r * (16 * kChunks) + 16 * sw);
+  }
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    const int r = i * kStep + lane / kChunks;
+    if (r < rows) *reinterpret_cast<uint4*>(out + r * pitch + 16 * c) = v[i];
+  }
+}
+
+// CH values (32 or 64) of each row from column x on, as fp32 or bf16; y: the warp's first row.
+template <int CH>
+__device__ __forceinline__ void put_values(const MmParams& p, const float (&v)[CH], uint8_t* stg, int x, int y, bool ok,
+                                           int lane) {
+  const int rows = ok ? min(32, p.M - y) : 0;
+  const int64_t at = static_cast<int64_t>(y) * p.ldy + x;
+  if (p.out == 1) {
+    uint32_t w[CH / 2];
+#pragma unroll
+    for (int i = 0; i < CH / 2; ++i) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    put_rows(w, stg, static_cast<uint8_t*>(p.y) + 2 * at, 2 * p.ldy, 2 * (p.N - x), rows, lane);
+  } else {
+#pragma unroll
+    for (int h = 0; h < CH; h += 32) {
+      uint32_t w[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[h + i]);
+      put_rows(w, stg, static_cast<uint8_t*>(p.y) + 4 * (at + h), 4 * p.ldy, 4 * (p.N - x - h), rows, lane);
+    }
+  }
+}
+
+// ACT: -1 plain, 0 SiLU-gated, 1 GELU-gated
+template <int BN, int ACT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<BN>::kThreads, 1)
+k_mm_pair(const __grid_constant__ MmParams p) {
+  using C = Pair<BN>;
+  constexpr bool GATED = ACT >= 0;
+  constexpr int kBN = GATED ? BN / 2 : BN;                           // output columns of a tile
+  static_assert(!GATED || BN == 256, "an 8-bit block is the 128 outputs of a gated tile");
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(align_up(reinterpret_cast<uintptr_t>(smem_raw), 1024));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem);                // used in the first CTA
+  uint64_t* empty = full + C::kStages;
+  uint64_t* acc_full = empty + C::kStages;
+  uint64_t* acc_free = acc_full + 2;                                 // used in the first CTA
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_free + 2);
+  uint8_t* ring = smem + C::kRingOff;
+  uint8_t* sfring = smem + C::kSfOff;
+  uint32_t* top = reinterpret_cast<uint32_t*>(smem + C::kTopOff);
+
+  const int warp = warp_index(), lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int MT = static_cast<int>(cdiv(p.M, 256)), NT = static_cast<int>(cdiv(p.N, kBN)), T = MT * NT;
+  const int KT = static_cast<int>(cdiv(p.K, kBlk));
+  const int first = static_cast<int>(blockIdx.x >> 1), step = static_cast<int>(gridDim.x >> 1);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+    for (int b = 0; b < 2; ++b) { mbar_init(&acc_full[b], 1); mbar_init(&acc_free[b], 16); }
+    fence_mbar_init();
+    prefetch_tmap(&p.tmap_w[0]);
+    if (GATED) prefetch_tmap(&p.tmap_w[1]);
+    prefetch_tmap(&p.tmap_x);
+  }
+  if (warp == 1) { tmem_alloc_pair(tmem_slot, 512); tmem_relinquish_pair(); }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();                                                    // both CTAs' barriers exist
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0 || warp == 10) {
+    const bool tokens = warp == 0;
+    const int w = GATED ? static_cast<int>(rank) : 0;                // gated: gate rows here, up rows there
+    if (tokens || !p.dependent) grid_dep_wait();                     // (see k_rows_mm)
+    if (tokens) grid_dep_launch();
+    const uint32_t one = elect_one();
+    const int ka = static_cast<int>(p.katoms), nb = static_cast<int>(cdiv(p.N, 128)) - 1;
+    const int xb = static_cast<int>(cdiv(p.M, 128)) - 1;
+    const CUtensorMap* map = tokens ? &p.tmap_x : &p.tmap_w[w];
+    const uint32_t ring0 = smem_u32(ring) + (tokens ? 0 : C::kATile);
+    const uint32_t sf0 = smem_u32(sfring) + (tokens ? 0 : 512);
+    const uint32_t bar0 = mapa_shared(smem_u32(&full[0]), 0), mine0 = smem_u32(&full[0]);
+    const uint32_t expect = tokens && rank == 0 ? one : 0u;
+    uint32_t off = 0, st = ring0, sf = sf0;
+    int s = 0;
+    uint32_t ph = 1;
+    int64_t it = 0;
+    bool ok = true;
+    for (int tile = first; tile < T && ok; tile += step) {
+      int mt, nt;
+      pair_tile(tile, MT, NT, mt, nt);
+      const int m0 = mt * 256 + 128 * static_cast<int>(rank);
+      const int n0 = GATED ? nt * 128 : nt * BN + BN / 2 * static_cast<int>(rank);
+      const int y = tokens ? m0 : n0;
+      // scale atoms by row group; a group past the last (its results are not stored) takes the last
+      const int xa = min(m0 / 128, xb) * ka, wa0 = (GATED ? nt : nt * BN / 128) * ka,
+                wa1 = (GATED ? nt : min(nt * BN / 128 + 1, nb)) * ka;
+      for (int kt = 0; kt < KT; ++kt, ++it) {
+        if (it >= C::kStages && !mbar_wait(&empty[s], ph, p.err, KQ_DEV_ERR_TIMEOUT_EMPTY)) {
+          ok = false;
+          break;
+        }
+        const bool atom = (kt & 3) == 0;
+        expect_tx_if(expect, mine0 + off, 2 * (C::kStageBytes + (atom ? C::kSfBytes : 0u)));
+        tma_load_pair_if(one, st, map, kt * kBlk, y, bar0 + off);
+        if (atom) {
+          if (tokens) {
+            tma_load_pair_if(one, sf, &p.tmap_sfx, 0, xa + (kt >> 2), bar0 + off);
+          } else {
+            tma_load_pair_if(one, sf, &p.tmap_sfw[0], 0, wa0 + (kt >> 2), bar0 + off);
+            if (C::kWAtoms > 1) tma_load_pair_if(one, sf + 512, &p.tmap_sfw[GATED ? 1 : 0], 0, wa1 + (kt >> 2), bar0 + off);
+          }
+        }
+        st += C::kStageBytes;
+        sf += C::kSfBytes;
+        off += 8;
+        if (++s == C::kStages) { s = 0; ph ^= 1u; off = 0; st = ring0; sf = sf0; }
+      }
+    }
+    // the first CTA's barriers count the loads of both; the peer leaves after the cluster barrier
+    // below, so after this wait
+    if (!ok && rank == 0 && one) drain_ring(full, C::kStages, it);
+  } else if (warp == 1) {
+    if (rank == 0) {
+      const uint32_t one = elect_one();
+      const uint64_t ad0 = sdesc_sw128_kmajor(smem_u32(ring)), bd0 = sdesc_sw128_kmajor(smem_u32(ring) + C::kATile);
+      const uint64_t sd0 = sdesc_plain_rows16(smem_u32(sfring));
+      uint64_t so = 0, sd = sd0;
+      uint32_t bar = smem_u32(empty), f = tmem + C::kSfCol + C::kSfSet * (C::kSets - 1);
+      int s = 0, local = 0, set = C::kSets - 1;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int tile = first; tile < T && ok; tile += step, ++local) {
+        const int buf = local & 1;
+        const int since = C::kShared && buf ? local - 1 : local - 2;  // tiles since acc_free[buf]'s first phase
+        if (since >= 0 && !mbar_wait_cluster(&acc_free[buf], (since >> 1) & 1, p.err, KQ_DEV_ERR_TIMEOUT_ACC)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + static_cast<uint32_t>(buf) * C::kAccStride;
+        uint32_t shift = 0;                                          // a tile may start in mid-atom
+        if (BN % 128 != 0) {
+          int mt, nt;
+          pair_tile(tile, MT, NT, mt, nt);
+          shift = static_cast<uint32_t>(nt * BN % 128) / 32u;
+        }
+        uint32_t acc = 0;
+        for (int kt = 0; kt < KT; ++kt) {
+          if (!mbar_wait(&full[s], ph, p.err, KQ_DEV_ERR_TIMEOUT_FULL)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t id = static_cast<uint32_t>(kt) & 3u;
+          if (id == 0) {
+            set = set + 1 == C::kSets ? 0 : set + 1;
+            f = tmem + C::kSfCol + C::kSfSet * set;
+            scale_cp_if<true>(one, f, sd);
+            scale_cp_if<true>(one, f + 4, sd + 32);
+            if (C::kWAtoms > 1) scale_cp_if<true>(one, f + 8, sd + 64);
+          }
+          const uint32_t idesc = idesc_mxf8(256, BN, 0) | (id << 4) | (id << 29);
+          const uint32_t fa = f | (id << 30);
+          // all four K steps of 32, the last k-tile's too: what lies past K was filled with zeros
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_mxf8_if<true>(one, d, ad0 + so + 2 * kk, bd0 + so + 2 * kk, idesc, fa, fa + 4 + shift, kk == 0 ? acc : 1u);
+          commit_if<true>(one, bar);
+          acc = 1;
+          so += C::kStageBytes >> 4;
+          sd += C::kSfBytes >> 4;
+          bar += 8;
+          if (++s == C::kStages) { s = 0; ph ^= 1u; so = 0; sd = sd0; bar = smem_u32(empty); }
+        }
+        commit_if<true>(one, smem_u32(&acc_full[buf]));
+      }
+    }
+  } else {
+    grid_dep_wait();
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    uint8_t* stg = smem + C::kStgOff + static_cast<uint32_t>(warp - 2) * C::kStgBytes;
+    const uint32_t free0 = mapa_shared(smem_u32(&acc_free[0]), 0);
+    if (GATED && p.out == 2 && blockIdx.x == 0 && threadIdx.x == 64) *p.oerr = 0u;
+    // Each warp of both CTAs frees an accumulator when it has read its columns (16 arrivals). Shared
+    // columns are the second half's of accumulator 0 and the first half's of 1: their owner frees
+    // the other accumulator after reading them, and its own after reading the rest; the first
+    // half's share of accumulator 1's first turn is free from the start.
+    if (C::kShared && half == 0 && lane == 0) mbar_arrive_cluster(free0 + 8);
+    int local = 0;
+    for (int tile = first; tile < T; tile += step, ++local) {
+      int mt, nt;
+      pair_tile(tile, MT, NT, mt, nt);
+      const int m0 = mt * 256 + 128 * static_cast<int>(rank) + 32 * q;
+      const int buf = local & 1;
+      const bool owner = half != buf;
+      const bool ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (local >> 1) & 1, p.err, KQ_DEV_ERR_TIMEOUT_ACC));
+      tc_fence_after();
+      const uint32_t tb = tmem + static_cast<uint32_t>(buf) * C::kAccStride + (static_cast<uint32_t>(32 * q) << 16);
+      auto release = [&](int b) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(free0 + 8u * static_cast<uint32_t>(b));
+      };
+      if (!GATED) {
+        // chunks of 64 (or 32) columns; the shared ones first: 192 .. 255 in the second half of
+        // accumulator 0, 0 .. 63 in the first of accumulator 1
+        constexpr int kCols = BN / 2, CH = kCols % 64 ? 32 : 64, kChunks = kCols / CH;
+        const int n0 = nt * BN + kCols * half;
+#pragma unroll 1
+        for (int c = 0; c < kChunks; ++c) {
+          const int col = CH * (C::kShared && buf == 0 && half == 1 ? kChunks - 1 - c : c);
+          uint32_t r[CH / 32][32];
+#pragma unroll
+          for (int h = 0; h < CH / 32; ++h) tmem_ld_32x32b_x32(tb + kCols * half + col + 32 * h, r[h]);
+          tmem_ld_wait();
+          if (C::kShared && owner) release(c == 0 ? buf ^ 1 : buf);
+          if (!C::kShared && c == kChunks - 1) release(buf);
+          float v[CH];
+#pragma unroll
+          for (int i = 0; i < CH; ++i) v[i] = __uint_as_float(r[i >> 5][i & 31]);
+          if (n0 + col < p.N) put_values(p, v, stg, n0 + col, m0, ok, lane);
+        }
+      } else {
+        // outputs 64 half .. 64 half + 63: the operand with the shared columns first (up in
+        // accumulator 0, the gate in 1), then the other
+        const uint32_t g0 = tb + 64 * half, u0 = g0 + 128;
+        float v[64];
+        {
+          uint32_t r[2][32];
+          tmem_ld_32x32b_x32(buf == 0 ? u0 : g0, r[0]);
+          tmem_ld_32x32b_x32((buf == 0 ? u0 : g0) + 32, r[1]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i >> 5][i & 31]);
+        }
+        if (owner) release(buf ^ 1);
+        uint32_t a = 0;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t r[32];
+          tmem_ld_32x32b_x32((buf == 0 ? g0 : u0) + 32 * c, r);
+          tmem_ld_wait();
+          if (owner && c == 1) release(buf);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float o = __uint_as_float(r[i]), f = v[32 * c + i];
+            v[32 * c + i] = gate_act<ACT>(buf == 0 ? o : f) * (buf == 0 ? f : o);
+          }
+        }
+        const int n0 = nt * 128 + 64 * half;
+        if (p.out != 2) {
+          put_values(p, v, stg, n0, m0, ok, lane);
+        } else {
+          // a block is the 128 outputs of a token in this tile: its largest value from both halves
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (n0 + i < p.N) a = max(a, abs_bits(v[i]));
+          top[128 * half + 32 * q + lane] = a;
+          asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");
+          a = max(a, top[128 * (half ^ 1) + 32 * q + lane]);
+          asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");
+          const uint32_t byte = scale_byte(a);
+          const float is = inv_scale(byte);
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            w[i] = e4m3x4(v[4 * i] * is, v[4 * i + 1] * is, v[4 * i + 2] * is, v[4 * i + 3] * is);
+          put_rows(w, stg, p.ocodes + static_cast<int64_t>(m0) * p.N + n0, p.N, p.N - n0, ok ? min(32, p.M - m0) : 0, lane);
+          if (ok && half == 0 && m0 + lane < p.M) p.osf[sf_offset(m0 + lane, nt, p.okatoms)] = static_cast<uint8_t>(byte);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();              // the peer's MMAs, loads and arrivals that reach into this CTA are over
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+template <int BN, int ACT>
+cudaError_t launch_pair_kernel(const MmParams& p, int sms, cudaStream_t st) {
+  using C = Pair<BN>;
+  auto fn = k_mm_pair<BN, ACT>;
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem));
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = cdiv(p.M, 256) * cdiv(p.N, ACT >= 0 ? BN / 2 : BN);
+  const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, p);
+}
+
+}  // namespace
+
+int pair_cols(int M, int N, int K, bool gated, int sms) {
+  if (M <= kRowsMaxM) return 0;
+  if (gated) return 256;
+  // ns of a pair's share of the tiles: per k-tile and per tile, as measured
+  const int64_t kt = cdiv(K, kBlk), mt = cdiv(M, 256), pairs = sms / 2;
+  const int64_t c256 = cdiv(mt * cdiv(N, 256), pairs) * (370 * kt + 1300);
+  const int64_t c192 = cdiv(mt * cdiv(N, 192), pairs) * (285 * kt + 650);
+  const int64_t c128 = cdiv(mt * cdiv(N, 128), pairs) * (215 * kt + 500);
+  return c128 < c192 && c128 < c256 ? 128 : c192 < c256 ? 192 : 256;
+}
+
+cudaError_t launch_pair(const MmParams& p, bool gated, int sms, cudaStream_t st) {
+  if (gated) return p.act == 0 ? launch_pair_kernel<256, 0>(p, sms, st) : launch_pair_kernel<256, 1>(p, sms, st);
+  switch (p.pairs) {
+    case 256: return launch_pair_kernel<256, -1>(p, sms, st);
+    case 192: return launch_pair_kernel<192, -1>(p, sms, st);
+    default: return launch_pair_kernel<128, -1>(p, sms, st);
+  }
+}
+
+}  // namespace fp8
+}  // namespace kq

@@ -10,24 +10,10 @@ namespace fp8 {
 
 namespace {
 
-__device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-}
-
-// Encodes the 8 values that each thread holds of a block shared by 16 neighbouring lanes
-// (lanes past a short last block hold zeros); `kb` is the block's index along K.
+// Encodes the 8 values that each thread holds of a block shared by 16 neighbouring lanes (lanes
+// without a chunk of the row hold zeros).
 __device__ __forceinline__ void encode8(const float (&v)[8], bool valid, int row, int chunk, const NormParams& p) {
-  uint32_t a = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) a = max(a, abs_bits(v[i]));
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
-  const uint32_t byte = scale_byte(a);
+  const uint32_t byte = block_byte(v);
   const float is = inv_scale(byte);
   if (!valid) return;
   uint2 c;
@@ -37,93 +23,145 @@ __device__ __forceinline__ void encode8(const float (&v)[8], bool valid, int row
   if ((chunk & 15) == 0) p.sf[sf_offset(row, chunk >> 4, p.katoms)] = static_cast<uint8_t>(byte);
 }
 
-// One CTA per token. A thread holds C chunks of 8 features (16 bytes of x); 16 neighbouring
-// threads share a scale.
+// Every row kernel starts behind the kernel before it, and lets the next one start only then: a
+// kernel that was started early thus knows that all but its direct predecessor have ended.
+__device__ __forceinline__ void enter(const NormParams& p) {
+  grid_dep_wait();
+  grid_dep_launch();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && threadIdx.y == 0) *p.err = 0u;
+}
+
+// The plain quantizer: kRowsC chunks of 8 features (16 bytes) per thread, loaded together;
+// blockDim.x threads along a row, blockDim.y rows.
+constexpr int kRowsC = 4;
+__global__ void __launch_bounds__(256) k_quant(const __grid_constant__ NormParams p) {
+  enter(p);
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  const int nch = row < p.M ? p.K / 8 : 0;
+  const int first = blockIdx.y * (kRowsC * blockDim.x) + threadIdx.x;
+  const uint4* x = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.x) + row * p.ldx);
+  uint4 u[kRowsC];
+#pragma unroll
+  for (int c = 0; c < kRowsC; ++c) {
+    const int ch = first + c * static_cast<int>(blockDim.x);
+    u[c] = ch < nch ? __ldcg(x + ch) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int c = 0; c < kRowsC; ++c) {
+    const int ch = first + c * static_cast<int>(blockDim.x);
+    float v[8];
+    unpack8(u[c], v);
+    encode8(v, ch < nch, static_cast<int>(row), ch, p);
+  }
+}
+
+// The norm: one CTA per token, C chunks of 8 features per thread, all loads before the first
+// store; 16 neighbouring threads share a scale.
 //   h = x + residual in fp32, rounded to the residual's type and kept there;
 //   r = 1 / sqrt(mean(h^2) + eps), the sum and the root in float64, rounded once to fp32;
 //   y = (h r) gamma, two fp32 products; then the block's scale and codes from y.
 // The float64 sum makes r, and so every code, independent of the summation order.
-template <int C, int RES, bool NORM>
-__global__ void __launch_bounds__(512) k_rows(const __grid_constant__ NormParams p) {
+template <int C, int RES>
+__global__ void __launch_bounds__(512) k_norm(const __grid_constant__ NormParams p) {
   __shared__ double part[16];
-  const int row = blockIdx.x;
-  const int T = blockDim.x;
-  const int nch = p.K / 8;
-  const int first = blockIdx.y * (T * C) + threadIdx.x;
-  if (p.err != nullptr && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.err = 0u;
-  grid_dep_launch();
-  const uint4* x = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.x) +
-                                                  static_cast<int64_t>(row) * p.ldx);
+  enter(p);
+  const int64_t row = blockIdx.x;
+  const int T = blockDim.x, nch = p.K / 8;
+  const uint4* x = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.x) + row * p.ldx);
+  uint4* rb = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.residual) + row * p.ldr);
+  float4* rf = reinterpret_cast<float4*>(static_cast<float*>(p.residual) + row * p.ldr);
+  uint4 u[C], r1[RES == 1 ? C : 1];
   float h[C][8];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int ch = threadIdx.x + c * T;
+    const bool valid = ch < nch;
+    u[c] = valid ? x[ch] : make_uint4(0, 0, 0, 0);
+    if (RES == 1) r1[c] = valid ? rb[ch] : make_uint4(0, 0, 0, 0);
+    if (RES == 2) {
+      const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+      const float4 r0 = valid ? rf[2 * ch] : z, r2 = valid ? rf[2 * ch + 1] : z;
+      h[c][0] = r0.x; h[c][1] = r0.y; h[c][2] = r0.z; h[c][3] = r0.w;
+      h[c][4] = r2.x; h[c][5] = r2.y; h[c][6] = r2.z; h[c][7] = r2.w;
+    }
+  }
   double sum = 0.0;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int ch = first + c * T;
+    const int ch = threadIdx.x + c * T;
     const bool valid = ch < nch;
-    uint4 u = make_uint4(0, 0, 0, 0);
-    if (valid) u = x[ch];
-    unpack8(u, h[c]);
-    if (RES == 1 && valid) {
-      uint4* rp = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.residual) +
-                                           static_cast<int64_t>(row) * p.ldr) + ch;
+    float v[8];
+    unpack8(u[c], v);
+    if (RES == 0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[c][i] = v[i];
+    }
+    if (RES == 1) {
       float r[8];
-      unpack8(*rp, r);
+      unpack8(r1[c], r);
       uint32_t o[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(h[c][2 * i] + r[2 * i], h[c][2 * i + 1] + r[2 * i + 1]);
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i] + r[2 * i], v[2 * i + 1] + r[2 * i + 1]);
         o[i] = *reinterpret_cast<const uint32_t*>(&b);
       }
       const uint4 ov = make_uint4(o[0], o[1], o[2], o[3]);
-      *rp = ov;
+      if (valid) rb[ch] = ov;
       unpack8(ov, h[c]);
     }
-    if (RES == 2 && valid) {
-      float4* rp = reinterpret_cast<float4*>(static_cast<float*>(p.residual) +
-                                             static_cast<int64_t>(row) * p.ldr) + 2 * ch;
-      const float4 r0 = rp[0], r1 = rp[1];
-      h[c][0] += r0.x; h[c][1] += r0.y; h[c][2] += r0.z; h[c][3] += r0.w;
-      h[c][4] += r1.x; h[c][5] += r1.y; h[c][6] += r1.z; h[c][7] += r1.w;
-      rp[0] = make_float4(h[c][0], h[c][1], h[c][2], h[c][3]);
-      rp[1] = make_float4(h[c][4], h[c][5], h[c][6], h[c][7]);
-    }
-    if (NORM) {
+    if (RES == 2) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fma(static_cast<double>(h[c][i]), static_cast<double>(h[c][i]), sum);
+      for (int i = 0; i < 8; ++i) h[c][i] = v[i] + h[c][i];
+      if (valid) {
+        rf[2 * ch] = make_float4(h[c][0], h[c][1], h[c][2], h[c][3]);
+        rf[2 * ch + 1] = make_float4(h[c][4], h[c][5], h[c][6], h[c][7]);
+      }
     }
-  }
-  float r = 1.f;
-  if (NORM) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
-    __syncthreads();
-    double s = 0.0;
-    for (int w = 0; w < (T >> 5); ++w) s += part[w];
-    r = static_cast<float>(1.0 / sqrt(s / static_cast<double>(p.K) + p.eps));
+    for (int i = 0; i < 8; ++i) sum = fma(static_cast<double>(h[c][i]), static_cast<double>(h[c][i]), sum);
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
+  __syncthreads();
+  double total = 0.0;
+  for (int w = 0; w < (T >> 5); ++w) total += part[w];
+  const float r = static_cast<float>(1.0 / sqrt(total / static_cast<double>(p.K) + p.eps));
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int ch = first + c * T;
+    const int ch = threadIdx.x + c * T;
     const bool valid = ch < nch;
-    if (NORM && valid) {
+    if (valid) {
       const float4* g = reinterpret_cast<const float4*>(p.gamma) + 2 * ch;
-      const float4 g0 = __ldg(g), g1 = __ldg(g + 1);
+      const float4 g0 = g[0], g1 = g[1];
       h[c][0] = h[c][0] * r * g0.x; h[c][1] = h[c][1] * r * g0.y;
       h[c][2] = h[c][2] * r * g0.z; h[c][3] = h[c][3] * r * g0.w;
       h[c][4] = h[c][4] * r * g1.x; h[c][5] = h[c][5] * r * g1.y;
       h[c][6] = h[c][6] * r * g1.z; h[c][7] = h[c][7] * r * g1.w;
     }
-    encode8(h[c], valid, row, ch, p);
+    encode8(h[c], valid, static_cast<int>(row), ch, p);
   }
 }
 
-template <int C, bool NORM>
-cudaError_t launch_rows_c(const NormParams& p, int res_kind, dim3 grid, int T, cudaStream_t st) {
-  if (!NORM || res_kind == 0) k_rows<C, 0, NORM><<<grid, T, 0, st>>>(p);
-  else if (res_kind == 1) k_rows<C, 1, NORM><<<grid, T, 0, st>>>(p);
-  else k_rows<C, 2, NORM><<<grid, T, 0, st>>>(p);
-  return cudaGetLastError();
+// All of these kernels wait for the kernel before them (griddepcontrol.wait) ahead of their
+// first access, so that their start may overlap its end.
+template <typename... A>
+cudaError_t launch_behind(void (*fn)(A...), dim3 grid, dim3 block, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+
+template <int C>
+cudaError_t launch_norm_c(const NormParams& p, int res_kind, dim3 grid, int T, cudaStream_t st) {
+  return launch_behind(res_kind == 0 ? k_norm<C, 0> : res_kind == 1 ? k_norm<C, 1> : k_norm<C, 2>, grid, dim3(T), st, p);
 }
 
 // One CTA per 128 (outputs) x 128 (inputs) piece of W [K, N]: transposed to K-major codes.
@@ -179,39 +217,53 @@ __global__ void k_act_scales(uint8_t* canon, int kb, int64_t count, uint8_t* sf,
   else canon[i] = *s;
 }
 
-// The values that codes stand for: 8 per thread.
+// The values that codes stand for: two chunks of 16 codes per thread (K is a multiple of 32, so a
+// chunk lies in one block), both loaded first.
 template <bool BF16>
-__global__ void __launch_bounds__(256) k_act_values(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ sf,
-                                                    int K, int64_t chunks, int64_t ka, void* __restrict__ out) {
+__global__ void __launch_bounds__(256) k_act_values(const uint8_t* codes, const uint8_t* sf, int K, int64_t chunks,
+                                                    int64_t ka, void* out) {
   grid_dep_wait();
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (i >= chunks) return;
-  const int per = K / 8;
-  const int64_t row = i / per;
-  const int ch = static_cast<int>(i - row * per);
-  const uint2 c = *reinterpret_cast<const uint2*>(codes + i * 8);
-  const float s = scale_value(sf[sf_offset(row, ch >> 4, ka)]);
-  const uint32_t w[2] = {c.x, c.y};
-  float v[8];
+  grid_dep_launch();
+  const uint32_t per = static_cast<uint32_t>(K) / 16;
+  int64_t at[2];
+  uint4 c[2];
+  float s[2];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    uint32_t h2;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)))));
-    const __half2 hh = *reinterpret_cast<const __half2*>(&h2);
-    v[2 * j] = __low2float(hh) * s;
-    v[2 * j + 1] = __high2float(hh) * s;
+  for (int k = 0; k < 2; ++k) {
+    const int64_t i = at[k] = (static_cast<int64_t>(blockIdx.x) * 2 + k) * 256 + threadIdx.x;
+    if (i >= chunks) continue;
+    const int64_t row = chunks <= 0xFFFFFFFFll ? static_cast<int64_t>(static_cast<uint32_t>(i) / per) : i / per;
+    c[k] = *reinterpret_cast<const uint4*>(codes + i * 16);
+    s[k] = scale_value(sf[sf_offset(row, (i - row * per) >> 3, ka)]);
   }
-  if (BF16) {
-    uint32_t o[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-      o[j] = *reinterpret_cast<const uint32_t*>(&b);
+  for (int k = 0; k < 2; ++k) {
+    if (at[k] >= chunks) continue;
+    const uint32_t w[4] = {c[k].x, c[k].y, c[k].z, c[k].w};
+    float v[16];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      uint32_t h2;
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)))));
+      const __half2 hh = *reinterpret_cast<const __half2*>(&h2);
+      v[2 * j] = __low2float(hh) * s[k];
+      v[2 * j + 1] = __high2float(hh) * s[k];
     }
-    reinterpret_cast<uint4*>(out)[i] = make_uint4(o[0], o[1], o[2], o[3]);
-  } else {
-    reinterpret_cast<float4*>(out)[2 * i] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(out)[2 * i + 1] = make_float4(v[4], v[5], v[6], v[7]);
+    if (BF16) {
+      uint32_t o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+        o[j] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      uint4* d = reinterpret_cast<uint4*>(out) + 2 * at[k];
+      d[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    } else {
+      float4* d = reinterpret_cast<float4*>(out) + 4 * at[k];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) d[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    }
   }
 }
 
@@ -220,18 +272,22 @@ __global__ void __launch_bounds__(256) k_act_values(const uint8_t* __restrict__ 
 cudaError_t launch_rows(const NormParams& p, bool norm, int res_kind, cudaStream_t st) {
   const int nch = p.K / 8;
   if (!norm) {
-    const int T = nch >= 256 ? 256 : static_cast<int>(align_up(nch, 32));
-    return launch_rows_c<1, false>(p, 0, dim3(p.M, static_cast<unsigned>(cdiv(nch, T))), T, st);
+    const int per = static_cast<int>(align_up(nch, 16));                 // whole blocks
+    const int want = static_cast<int>(align_up(cdiv(per, kRowsC), 16));
+    const int tx = want < 128 ? want : 128;
+    const int ty = 256 / tx - (256 / tx * tx % 32 ? 1 : 0);              // whole warps
+    const dim3 grid(static_cast<unsigned>(cdiv(p.M, ty)), static_cast<unsigned>(cdiv(per, kRowsC * tx)));
+    return launch_behind(k_quant, grid, dim3(tx, ty), st, p);
   }
   int C = 1;
-  while (C < 8 && nch > 512 * C) C *= 2;
+  while (C < 8 && nch > 256 * C) C *= 2;
   const int T = static_cast<int>(align_up(cdiv(nch, C), 32));
   const dim3 grid(p.M);
   switch (C) {
-    case 1: return launch_rows_c<1, true>(p, res_kind, grid, T, st);
-    case 2: return launch_rows_c<2, true>(p, res_kind, grid, T, st);
-    case 4: return launch_rows_c<4, true>(p, res_kind, grid, T, st);
-    default: return launch_rows_c<8, true>(p, res_kind, grid, T, st);
+    case 1: return launch_norm_c<1>(p, res_kind, grid, T, st);
+    case 2: return launch_norm_c<2>(p, res_kind, grid, T, st);
+    case 4: return launch_norm_c<4>(p, res_kind, grid, T, st);
+    default: return launch_norm_c<8>(p, res_kind, grid, T, st);
   }
 }
 
@@ -257,11 +313,9 @@ cudaError_t launch_act_scales(uint8_t* canonical, int K, int M, uint8_t* sf, boo
 
 cudaError_t launch_act_values(const uint8_t* codes, const uint8_t* sf, int K, int M, void* values, bool bf16,
                               cudaStream_t st) {
-  const int64_t chunks = static_cast<int64_t>(M) * (K / 8);
-  const unsigned grid = static_cast<unsigned>(cdiv(chunks, 256));
-  if (bf16) k_act_values<true><<<grid, 256, 0, st>>>(codes, sf, K, chunks, katoms(K), values);
-  else k_act_values<false><<<grid, 256, 0, st>>>(codes, sf, K, chunks, katoms(K), values);
-  return cudaGetLastError();
+  const int64_t chunks = static_cast<int64_t>(M) * (K / 16);
+  return launch_behind(bf16 ? k_act_values<true> : k_act_values<false>, dim3(static_cast<unsigned>(cdiv(chunks, 512))),
+                       dim3(256), st, codes, sf, K, chunks, katoms(K), values);
 }
 
 }  // namespace fp8
