@@ -353,6 +353,39 @@ def test_ffn_is_its_parts(cuda_device, M, K, N, res):
     assert err <= np.sqrt(32 * d) / 8 + 1e-6
 
 
+@pytest.mark.parametrize("M", [3, 70])
+def test_buffers_on_16_byte_boundaries(cuda_device, M):
+    """Every device pointer 16 bytes past a 256-byte boundary gives the same results."""
+    import torch
+    import w4a4_post_quantization_token_b200 as kq
+    K, N = 288, 160
+
+    def off(t):
+        raw = torch.zeros(t.numel() * t.element_size() + 16, dtype=torch.uint8, device="cuda")
+        v = raw[16:].view(t.dtype).view(t.shape)
+        assert v.data_ptr() % 256 == 16
+        return v.copy_(t)
+
+    got = []
+    for move in (lambda t: t, off):
+        X, R, g = move(tokens(M, K, 1).cuda()), move(torch.ones(M, K, device="cuda")), move(torch.full((K,), 0.5, device="cuda"))
+        L = kq.Fp8Layer(K, N)
+        w = move(buf(kq.fp8_weights_bytes(L)))
+        kq.fp8_prepare_weights(L, move(weight(K, N, 2).cuda()), w)
+        act = move(buf(kq.fp8_act_bytes(K, M)))
+        V, F = move(torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")), move(torch.zeros(M, K, device="cuda"))
+        Y, Z = move(torch.zeros(M, N, device="cuda")), move(torch.zeros(M, N, dtype=torch.bfloat16, device="cuda"))
+        kq.fp8_quantize_act(X, act)
+        kq.fp8_act_unpack(K, act, M, values=V)
+        kq.fp8_rmsnorm_act(X, g, EPS, act, residual=R)
+        kq.fp8_act_unpack(K, act, M, values=F)
+        kq.fp8_gemm(L, w, act, M, Y)
+        kq.fp8_linear(L, w, X, Z, act, kq.OUT_BF16)
+        got.append([t.clone() for t in (V, R, F, Y, Z)])
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
 def test_ffn_without_norm(cuda_device):
     import torch
     import w4a4_post_quantization_token_b200 as kq

@@ -401,9 +401,9 @@ int pair_cols(int M, int N, int K, bool gated, int sms) {
   if (gated) return 256;
   // ns of a pair's share of the tiles: per k-tile and per tile, as measured
   const int64_t kt = cdiv(K, kBlk), mt = cdiv(M, 256), pairs = sms / 2;
-  const int64_t c256 = cdiv(mt * cdiv(N, 256), pairs) * (370 * kt + 1300);
-  const int64_t c192 = cdiv(mt * cdiv(N, 192), pairs) * (285 * kt + 650);
-  const int64_t c128 = cdiv(mt * cdiv(N, 128), pairs) * (215 * kt + 500);
+  const int64_t c256 = cdiv(mt * cdiv(N, 256), pairs) * (340 * kt + 900);
+  const int64_t c192 = cdiv(mt * cdiv(N, 192), pairs) * (265 * kt + 550);
+  const int64_t c128 = cdiv(mt * cdiv(N, 128), pairs) * (200 * kt + 450);
   return c128 < c192 && c128 < c256 ? 128 : c192 < c256 ? 192 : 256;
 }
 

@@ -31,27 +31,70 @@ __device__ __forceinline__ void enter(const NormParams& p) {
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && threadIdx.y == 0) *p.err = 0u;
 }
 
-// The plain quantizer: kRowsC chunks of 8 features (16 bytes) per thread, loaded together;
-// blockDim.x threads along a row, blockDim.y rows.
+// 32 bytes as one access where the caller's rows allow it (a warp's 16-byte accesses 32 bytes apart
+// would fetch each sector twice), else as two.
+__device__ __forceinline__ void load32(const void* p, bool wide, uint32_t (&u)[8]) {
+  if (wide) {
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+                 : "l"(p) : "memory");
+  } else {
+    const uint4 a = static_cast<const uint4*>(p)[0], b = static_cast<const uint4*>(p)[1];
+    u[0] = a.x; u[1] = a.y; u[2] = a.z; u[3] = a.w;
+    u[4] = b.x; u[5] = b.y; u[6] = b.z; u[7] = b.w;
+  }
+}
+__device__ __forceinline__ void store32(void* p, bool wide, const uint32_t* u) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};"
+                 ::"r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "l"(p)
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(u[4], u[5], u[6], u[7]);
+  }
+}
+
+// The plain quantizer: kRowsC chunks of 16 features (32 bytes) per thread, loaded together; 8
+// neighbouring threads share a scale; blockDim.x threads along a row, blockDim.y rows.
 constexpr int kRowsC = 4;
-__global__ void __launch_bounds__(256) k_quant(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(256) k_quant(const __grid_constant__ NormParams p, bool wide) {
   enter(p);
   const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
-  const int nch = row < p.M ? p.K / 8 : 0;
+  const int nch = row < p.M ? p.K / 16 : 0;
   const int first = blockIdx.y * (kRowsC * blockDim.x) + threadIdx.x;
-  const uint4* x = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.x) + row * p.ldx);
-  uint4 u[kRowsC];
+  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x) + row * p.ldx;
+  uint32_t u[kRowsC][8];
 #pragma unroll
   for (int c = 0; c < kRowsC; ++c) {
     const int ch = first + c * static_cast<int>(blockDim.x);
-    u[c] = ch < nch ? __ldcg(x + ch) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[c][i] = 0;
+    if (ch < nch) load32(x + 16 * ch, wide, u[c]);
   }
 #pragma unroll
   for (int c = 0; c < kRowsC; ++c) {
     const int ch = first + c * static_cast<int>(blockDim.x);
-    float v[8];
-    unpack8(u[c], v);
-    encode8(v, ch < nch, static_cast<int>(row), ch, p);
+    float v[16];
+    uint32_t a = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[2 * i] = __uint_as_float(u[c][i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[c][i] & 0xFFFF0000u);
+      a = max(a, max(abs_bits(v[2 * i]), abs_bits(v[2 * i + 1])));
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+    const uint32_t byte = scale_byte(a);
+    const float is = inv_scale(byte);
+    if (ch >= nch) continue;
+    uint4 o;
+    o.x = e4m3x4(v[0] * is, v[1] * is, v[2] * is, v[3] * is);
+    o.y = e4m3x4(v[4] * is, v[5] * is, v[6] * is, v[7] * is);
+    o.z = e4m3x4(v[8] * is, v[9] * is, v[10] * is, v[11] * is);
+    o.w = e4m3x4(v[12] * is, v[13] * is, v[14] * is, v[15] * is);
+    *reinterpret_cast<uint4*>(p.codes + row * p.K + 16 * ch) = o;
+    if ((ch & 7) == 0) p.sf[sf_offset(row, ch >> 3, p.katoms)] = static_cast<uint8_t>(byte);
   }
 }
 
@@ -217,53 +260,46 @@ __global__ void k_act_scales(uint8_t* canon, int kb, int64_t count, uint8_t* sf,
   else canon[i] = *s;
 }
 
-// The values that codes stand for: two chunks of 16 codes per thread (K is a multiple of 32, so a
-// chunk lies in one block), both loaded first.
+// The values that codes stand for: two chunks of 32 codes per thread (K is a multiple of 32, so a
+// chunk lies in one block), both loaded first. `wide`: 32-byte accesses to the codes (1), the
+// values (2).
 template <bool BF16>
 __global__ void __launch_bounds__(256) k_act_values(const uint8_t* codes, const uint8_t* sf, int K, int64_t chunks,
-                                                    int64_t ka, void* out) {
+                                                    int64_t ka, uint8_t* out, int wide) {
   grid_dep_wait();
   grid_dep_launch();
-  const uint32_t per = static_cast<uint32_t>(K) / 16;
+  const uint32_t per = static_cast<uint32_t>(K) / 32;
   int64_t at[2];
-  uint4 c[2];
+  uint32_t c[2][8];
   float s[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int64_t i = at[k] = (static_cast<int64_t>(blockIdx.x) * 2 + k) * 256 + threadIdx.x;
     if (i >= chunks) continue;
     const int64_t row = chunks <= 0xFFFFFFFFll ? static_cast<int64_t>(static_cast<uint32_t>(i) / per) : i / per;
-    c[k] = *reinterpret_cast<const uint4*>(codes + i * 16);
-    s[k] = scale_value(sf[sf_offset(row, (i - row * per) >> 3, ka)]);
+    load32(codes + i * 32, wide & 1, c[k]);
+    s[k] = scale_value(sf[sf_offset(row, (i - row * per) >> 2, ka)]);
   }
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     if (at[k] >= chunks) continue;
-    const uint32_t w[4] = {c[k].x, c[k].y, c[k].z, c[k].w};
-    float v[16];
+    uint32_t o[BF16 ? 16 : 32];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 16; ++j) {
       uint32_t h2;
-      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)))));
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(c[k][j >> 1] >> (16 * (j & 1)))));
       const __half2 hh = *reinterpret_cast<const __half2*>(&h2);
-      v[2 * j] = __low2float(hh) * s[k];
-      v[2 * j + 1] = __high2float(hh) * s[k];
-    }
-    if (BF16) {
-      uint32_t o[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+      const float lo = __low2float(hh) * s[k], hi = __high2float(hh) * s[k];
+      if (BF16) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
         o[j] = *reinterpret_cast<const uint32_t*>(&b);
+      } else {
+        o[2 * j] = __float_as_uint(lo);
+        o[2 * j + 1] = __float_as_uint(hi);
       }
-      uint4* d = reinterpret_cast<uint4*>(out) + 2 * at[k];
-      d[0] = make_uint4(o[0], o[1], o[2], o[3]);
-      d[1] = make_uint4(o[4], o[5], o[6], o[7]);
-    } else {
-      float4* d = reinterpret_cast<float4*>(out) + 4 * at[k];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) d[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
     }
+#pragma unroll
+    for (int j = 0; j < (BF16 ? 2 : 4); ++j) store32(out + (at[k] * (BF16 ? 2 : 4) + j) * 32, wide & 2, o + 8 * j);
   }
 }
 
@@ -272,12 +308,13 @@ __global__ void __launch_bounds__(256) k_act_values(const uint8_t* codes, const 
 cudaError_t launch_rows(const NormParams& p, bool norm, int res_kind, cudaStream_t st) {
   const int nch = p.K / 8;
   if (!norm) {
-    const int per = static_cast<int>(align_up(nch, 16));                 // whole blocks
+    const int per = static_cast<int>(align_up(p.K / 16, 8));             // whole blocks
     const int want = static_cast<int>(align_up(cdiv(per, kRowsC), 16));
     const int tx = want < 128 ? want : 128;
     const int ty = 256 / tx - (256 / tx * tx % 32 ? 1 : 0);              // whole warps
     const dim3 grid(static_cast<unsigned>(cdiv(p.M, ty)), static_cast<unsigned>(cdiv(per, kRowsC * tx)));
-    return launch_behind(k_quant, grid, dim3(tx, ty), st, p);
+    const bool wide = (reinterpret_cast<uintptr_t>(p.x) | static_cast<uintptr_t>(p.ldx * 2)) % 32 == 0;
+    return launch_behind(k_quant, grid, dim3(tx, ty), st, p, wide);
   }
   int C = 1;
   while (C < 8 && nch > 256 * C) C *= 2;
@@ -313,9 +350,10 @@ cudaError_t launch_act_scales(uint8_t* canonical, int K, int M, uint8_t* sf, boo
 
 cudaError_t launch_act_values(const uint8_t* codes, const uint8_t* sf, int K, int M, void* values, bool bf16,
                               cudaStream_t st) {
-  const int64_t chunks = static_cast<int64_t>(M) * (K / 16);
+  const int64_t chunks = static_cast<int64_t>(M) * (K / 32);
+  const int wide = (reinterpret_cast<uintptr_t>(codes) % 32 == 0 ? 1 : 0) | (reinterpret_cast<uintptr_t>(values) % 32 == 0 ? 2 : 0);
   return launch_behind(bf16 ? k_act_values<true> : k_act_values<false>, dim3(static_cast<unsigned>(cdiv(chunks, 512))),
-                       dim3(256), st, codes, sf, K, chunks, katoms(K), values);
+                       dim3(256), st, codes, sf, K, chunks, katoms(K), static_cast<uint8_t*>(values), wide);
 }
 
 }  // namespace fp8
