@@ -414,8 +414,6 @@ def _rows(t, dtypes, rows: int | None, width: int, name: str) -> int:
     """Checks a matrix whose rows may be a pitch apart and returns the pitch."""
     if t is None:
         raise ValueError(f"{name} is required")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
     shape = t.shape
@@ -428,15 +426,30 @@ def _rows(t, dtypes, rows: int | None, width: int, name: str) -> int:
     return pitch if shape[0] > 1 else width
 
 
+def _flat(t, dtype, numel: int, name: str):
+    """Checks a contiguous tensor of at least numel elements (its device: _fp8_run)."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.numel() < numel:
+        raise ValueError(f"{name} has {t.numel()} elements, needs {numel}")
+    return t
+
+
 def _fp8_run(fn, where: str, stream, tensors, *args) -> None:
-    """Calls fn(*args, stream) on the device of `tensors`, which must all be on one device, and
-    on `stream` or that device's current stream."""
+    """Calls fn(*args, stream) on the device of `tensors`, which must all be on one CUDA device,
+    and on `stream` or that device's current stream."""
     import torch
     dev = -1
     for t in tensors:
         if t is not None:
             d = t.get_device()
-            if dev >= 0 and d != dev:
+            if d < 0:
+                raise ValueError(f"{where}: every tensor must be a CUDA tensor")
+            if d != dev and dev >= 0:
                 raise ValueError(f"{where}: tensors are on different devices")
             dev = d
     if stream is None:
@@ -445,7 +458,7 @@ def _fp8_run(fn, where: str, stream, tensors, *args) -> None:
         raise ValueError(f"{where}: the stream is of another device than the tensors")
     else:
         raw = stream.cuda_stream
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         status = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
@@ -476,14 +489,14 @@ def _fp8_weights(layer: Fp8Layer, weights):
     import torch
     if layer._weights_bytes == 0:
         raise ValueError(f"unsupported 8-bit layer K={layer.K} N={layer.N}")
-    return _need(weights, torch.uint8, layer._weights_bytes, "weights")
+    return _flat(weights, torch.uint8, layer._weights_bytes, "weights")
 
 
 def _e4m3(t, numel: int, name: str):
     import torch
     if t is not None and t.dtype == torch.float8_e4m3fn:
         t = t.view(torch.uint8)
-    return _need(t, torch.uint8, numel, name)
+    return _flat(t, torch.uint8, numel, name)
 
 
 def fp8_prepare_weights(layer: Fp8Layer, W, weights, W_up=None, stream=None) -> None:
@@ -492,7 +505,7 @@ def fp8_prepare_weights(layer: Fp8Layer, W, weights, W_up=None, stream=None) -> 
     _fp8_pair(layer, W_up, "W_up")
     _fp8_weights(layer, weights)
     for t, name in ((W, "W"), (W_up, "W_up"))[:1 + layer.gated]:
-        _need(t, torch.bfloat16, layer.K * layer.N, name)
+        _flat(t, torch.bfloat16, layer.K * layer.N, name)
     _fp8_run(lib.kq_fp8_prepare_weights, "kq_fp8_prepare_weights", stream, (W, W_up, weights), layer.desc, _ptr(W),
              _ptr(W_up), _ptr(weights))
 
@@ -506,7 +519,7 @@ def _fp8_parts(layer: Fp8Layer, codes, scales, up_codes, up_scales, optional: bo
             continue
         if i > 1 and not layer.gated:
             raise ValueError(f"{name} goes with gated layers only")
-        parts[i] = _need(t, torch.uint8, ns, name) if i % 2 else _e4m3(t, n, name)
+        parts[i] = _flat(t, torch.uint8, ns, name) if i % 2 else _e4m3(t, n, name)
     return parts
 
 
@@ -529,7 +542,7 @@ def fp8_weights_unpack(layer: Fp8Layer, weights, codes=None, scales=None, up_cod
 
 def _fp8_act(act, K: int, M: int, name: str = "act"):
     import torch
-    return _need(act, torch.uint8, fp8_act_bytes(K, M), name)
+    return _flat(act, torch.uint8, fp8_act_bytes(K, M), name)
 
 
 def fp8_quantize_act(X, act, stream=None) -> None:
@@ -545,7 +558,7 @@ def fp8_quantize_act(X, act, stream=None) -> None:
 def _fp8_norm(gamma, residual, M: int, K: int):
     """(residual pitch, residual dtype) after the checks."""
     import torch
-    _need(gamma, torch.float32, K, "gamma")
+    _flat(gamma, torch.float32, K, "gamma")
     if residual is None:
         return 0, OUT_F32
     ldr = _rows(residual, (torch.bfloat16, torch.float32), M, K, "residual")
@@ -567,7 +580,7 @@ def fp8_rmsnorm_act(X, gamma, eps: float, act, residual=None, stream=None) -> No
 def fp8_act_pack(K: int, codes, scales, M: int, act, stream=None) -> None:
     import torch
     codes = _e4m3(codes, M * K, "codes")
-    _need(scales, torch.uint8, M * -(-K // 128), "scales")
+    _flat(scales, torch.uint8, M * -(-K // 128), "scales")
     _fp8_act(act, K, M)
     _fp8_run(lib.kq_fp8_act_pack, "kq_fp8_act_pack", stream, (codes, scales, act), int(K), _ptr(codes),
              _ptr(scales), int(M), _ptr(act), act.numel())
@@ -582,10 +595,10 @@ def fp8_act_unpack(K: int, act, M: int, codes=None, scales=None, values=None, st
     if codes is not None:
         codes = _e4m3(codes, M * K, "codes")
     if scales is not None:
-        _need(scales, torch.uint8, M * -(-K // 128), "scales")
+        _flat(scales, torch.uint8, M * -(-K // 128), "scales")
     if values is not None:
         vdt = OUT_BF16 if values.dtype == torch.bfloat16 else OUT_F32
-        _need(values, torch.bfloat16 if vdt == OUT_BF16 else torch.float32, M * K, "values")
+        _flat(values, torch.bfloat16 if vdt == OUT_BF16 else torch.float32, M * K, "values")
     _fp8_run(lib.kq_fp8_act_unpack, "kq_fp8_act_unpack", stream, (act, codes, scales, values), int(K), _ptr(act),
              int(M), _ptr(codes), _ptr(scales), _ptr(values), vdt)
 
@@ -633,10 +646,9 @@ def fp8_ffn(gated: Fp8Layer, gated_weights, down: Fp8Layer, down_weights, X, gam
     M = X.shape[0]
     _fp8_weights(gated, gated_weights)
     _fp8_weights(down, down_weights)
-    need = fp8_ffn_bytes(gated, down, M)
-    if need == 0:
+    if not gated.gated or down.gated or down.K != gated.N or M < 1:
         raise ValueError("fp8_ffn takes a gated layer and a plain one with K equal to its N, and M >= 1")
-    _need(ws, torch.uint8, need, "ws")
+    _flat(ws, torch.uint8, fp8_act_bytes(gated.K, M) + fp8_act_bytes(gated.N, M), "ws")
     ldx = _rows(X, (torch.bfloat16,), None, gated.K, "X")
     if gamma is None and residual is not None:
         raise ValueError("residual needs gamma")
