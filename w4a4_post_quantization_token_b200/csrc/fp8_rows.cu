@@ -50,12 +50,16 @@ struct Rows {
   static constexpr uint32_t kSfOff = kProducts * kABytes + (FUSED ? 0 : kBBytes);   // scale atoms: weights, tokens
   static constexpr uint32_t kSfAtoms = kProducts + (FUSED ? 0 : 1);
   static constexpr uint32_t kStageBytes = kSfOff + (kSfAtoms > 2 ? 2048 : 1024);
-  // Few tokens, one product: two CTAs fit on an SM, so that the next product's weights arrive
-  // while this one ends. Otherwise the ring takes the SM: stages are large, and fewer than four
-  // in flight do not cover the latency of a load.
-  static constexpr bool kHalf = BT <= 32 && !GATED && !FUSED;
   static constexpr uint32_t kXBytes = FUSED ? 64 * 1024 : 0;               // encoded activations, at most
-  static constexpr int kStages = FUSED ? (GATED ? 4 : 5) : ((kHalf ? 110 : 216) * 1024 - 2048) / kStageBytes;
+  // Partials received in the exchange: [split][product][four tokens of the share][128 features] x
+  // 16 bytes. Up to 16 tokens they have room of their own; beyond, they go over the ring once the
+  // cluster's MMAs are done, which takes a cluster barrier more.
+  static constexpr bool kOwnPart = BT <= 16;
+  static constexpr uint32_t kPartBytes = kProducts * (kOwnPart ? kMaxSplits : BT / 4 + kMaxSplits) * 2048;
+  // As many stages as an SM holds, 9 at most (scale sets, below): every k-tile of a small share is
+  // under way at once.
+  static constexpr uint32_t kRoom = 226 * 1024 - 2048 - kXBytes - (FUSED ? 5120 : 0) - (kOwnPart ? kPartBytes : 0);
+  static constexpr int kStages = kRoom / kStageBytes < 9 ? kRoom / kStageBytes : 9;
   static constexpr uint32_t kRingBytes = kStages * kStageBytes;
   // accumulators 64 columns apart, then 3 scale sets of 16 columns
   static constexpr uint32_t kSfCol = kProducts * 64;
@@ -64,17 +68,16 @@ struct Rows {
   // at both ends of the share)
   static constexpr int kMaxShare = FUSED ? static_cast<int>(kXBytes / kBBytes) : 1 << 30;
   static constexpr uint32_t smem(int share) {
-    return 2048 + kRingBytes + (FUSED ? share * kBBytes + (share / 4 + 2) * 512 : 0);
+    return 2048 + kRingBytes + (kOwnPart ? kPartBytes : 0) + (FUSED ? share * kBBytes + (share / 4 + 2) * 512 : 0);
   }
   static_assert(kStages >= 3 && kStageBytes % 1024 == 0 && BT <= 64, "ring");
   static_assert(smem(FUSED ? kMaxShare : 0) + 1024 <= 232448, "shared memory");
   // A scale set is rewritten three atoms later, 9 k-tiles at least after its last use: those
   // MMAs have freed the stage that the new atom landed in.
   static_assert(kStages <= 9, "scale sets");
-  // partials received: [split][product][four tokens of the share][128 features] x 16 bytes
-  static_assert(kProducts * (BT / 4 + kMaxSplits) * 2048 <= kRingBytes, "exchange over the ring");
+  static_assert(kPartBytes <= kRingBytes, "exchange over the ring");
   // The CTAs of a cluster wait for one another, so that none may wait for TMEM columns which a
-  // CTA of another cluster on its SM holds.
+  // CTA of another cluster on its SM holds: columns for two.
   static_assert(kTmemCols <= 256, "two CTAs per SM");
 };
 
@@ -168,7 +171,8 @@ __global__ void __launch_bounds__(Rows<BT, GATED, FUSED>::kThreads) k_rows_mm(co
   const int KT = static_cast<int>(cdiv(p.K, kBlk));
   const int splits = static_cast<int>(gridDim.z), rank = static_cast<int>(blockIdx.z);   // a cluster along z
   const int kt0 = KT * rank / splits, n_kt = KT * (rank + 1) / splits - kt0;
-  uint8_t* xcodes = ring + C::kRingBytes;                                // FUSED: encoded share, its scales
+  float4* part = reinterpret_cast<float4*>(C::kOwnPart ? ring + C::kRingBytes : ring);
+  uint8_t* xcodes = ring + C::kRingBytes + (C::kOwnPart ? C::kPartBytes : 0);   // FUSED: encoded share, its scales
   uint8_t* xsf = xcodes + n_kt * C::kBBytes;
 
   if (threadIdx.x == 0) {
@@ -186,6 +190,8 @@ __global__ void __launch_bounds__(Rows<BT, GATED, FUSED>::kThreads) k_rows_mm(co
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  // kOwnPart: the others may store into this CTA's room once it has started, which they learn here
+  if (C::kOwnPart && splits > 1) cluster_arrive();
   if (warp == 0) {
     // The kernel that writes the activations is the one before this in the stream, and what ran
     // before that one has ended (`dependent`): the weights may be read without a wait.
@@ -297,8 +303,9 @@ __global__ void __launch_bounds__(Rows<BT, GATED, FUSED>::kThreads) k_rows_mm(co
   if (splits > 1) {
     // tokens go by fours; the share of split d: fours [Q d / splits, Q (d + 1) / splits)
     const int Q = (tokens + 3) / 4, cap = (Q + splits - 1) / splits;
-    float4* part = reinterpret_cast<float4*>(ring);
-    cluster_sync();                                        // every CTA's ring has been consumed
+    __syncwarp();
+    if (C::kOwnPart) cluster_wait();
+    else cluster_sync();                                   // every CTA's ring has been consumed
     if (epi) {
       const uint32_t mine = smem_u32(part) + 16u * static_cast<uint32_t>(rank * C::kProducts * cap * 128 + 32 * q + lane);
       int d = 0, q0 = 0, q1 = Q / splits;
