@@ -244,7 +244,8 @@ SHAPES = [(1, 32, 16), (1, 4096, 256), (3, 96, 48), (16, 512, 128), (17, 544, 14
           (64, 640, 128), (65, 2080, 256), (127, 160, 272), (128, 384, 128), (129, 1024, 144), (200, 12288, 160),
           (257, 1152, 528), (300, 96, 1040), (520, 736, 784), (1, 12288, 1040), (5, 8192, 640),
           (2100, 160, 2320), (1300, 640, 4112),         # several tiles for each CTA pair
-          (20, 2304, 9488), (31, 12288, 144), (16, 160, 272)]
+          (20, 2304, 9488), (31, 12288, 144), (16, 160, 272),
+          (65, 4096, 400), (100, 2080, 1936), (300, 1120, 144), (256, 12288, 528), (512, 8192, 656)]   # K shared by pairs
 
 
 @pytest.mark.parametrize("out", ["f32", "bf16"])
@@ -276,7 +277,7 @@ def gated_bound(z, u, zerr, uerr, kind):
 @pytest.mark.parametrize("kind", ["silu", "gelu"])
 @pytest.mark.parametrize("M,K,N", [(1, 32, 16), (2, 4096, 128), (16, 160, 144), (20, 512, 272), (64, 1152, 256),
                                    (65, 96, 400), (130, 2080, 272), (300, 640, 528), (1, 8192, 640), (1100, 160, 2080),
-                                   (700, 544, 4016)])
+                                   (700, 544, 4016), (100, 4096, 528), (257, 2080, 160), (300, 8192, 800)])
 def test_gated(cuda_device, M, K, N, kind):
     import torch
     import w4a4_post_quantization_token_b200 as kq

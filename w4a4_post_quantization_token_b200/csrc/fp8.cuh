@@ -152,6 +152,7 @@ struct MmParams {
   int64_t okatoms;
   uint32_t* oerr;
   int pairs;                  // weight rows of k_mm_pair's tile, 0: k_rows_mm
+  int splits;                 // k_mm_pair: pairs that share K
   int dependent;              // launched as a programmatic dependent of the kernel that writes
                               //   the activations, whose predecessors had ended
   uint32_t* err;
@@ -167,9 +168,11 @@ cudaError_t launch_act_values(const uint8_t* codes, const uint8_t* sf, int K, in
 struct Device { int sms, device; };
 
 constexpr int kRowsMaxM = 64;                // tokens that k_rows_mm takes; more go to k_mm_pair
-// Weight rows of k_mm_pair's tile, 0 where k_rows_mm is taken; the box height of MmParams::tmap_w
-// is half of them (128 for k_rows_mm).
-int pair_cols(int M, int N, int K, bool gated, int sms);
+constexpr int kMaxDevices = 64;              // whose cluster limits are kept
+// Weight rows of k_mm_pair's tile, 0 where k_rows_mm is taken, and the pairs that share K. The box
+// height of MmParams::tmap_w is half of the rows (128 for k_rows_mm).
+struct PairShape { int cols, splits; };
+PairShape pair_shape(int M, int N, int K, bool gated, const Device& d);
 cudaError_t launch_pair(const MmParams& p, bool gated, int sms, cudaStream_t st);
 // token tile of k_rows_mm (the box height of MmParams::tmap_x; 128 for k_mm_pair)
 int rows_token_tile(int M);

@@ -88,7 +88,9 @@ kq_status run_mm(const kq_fp8_desc* d, const void* weights, uint8_t* act, int32_
   std::memset(&p, 0, sizeof(p));
   const uint64_t K = static_cast<uint64_t>(d->K);
   const fp8::Device dev = {di.sms, di.device};
-  p.pairs = fp8::pair_cols(M, d->N, d->K, d->gated != 0, di.sms);
+  const fp8::PairShape shape = fp8::pair_shape(M, d->N, d->K, d->gated != 0, dev);
+  p.pairs = shape.cols;
+  p.splits = shape.splits;
   const uint32_t wrows = p.pairs ? static_cast<uint32_t>(p.pairs / 2) : 128;
   for (int i = 0; i < 1 + d->gated; ++i) {
     if (!make_tmap(&p.tmap_w[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, w + W.codes[i], K, static_cast<uint64_t>(d->N), K,

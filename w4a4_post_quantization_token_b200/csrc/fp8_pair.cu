@@ -18,6 +18,8 @@
 // when those are out, some 1800 cycles after the last MMA.
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "fp8.cuh"
 #include "sm100_fp8.cuh"
 
@@ -25,6 +27,7 @@ namespace kq {
 namespace fp8 {
 
 namespace {
+
 
 template <int BN>
 struct Pair {
@@ -120,14 +123,39 @@ __device__ __forceinline__ void put_values(const MmParams& p, const float (&v)[C
   }
 }
 
-// ACT: -1 plain, 0 SiLU-gated, 1 GELU-gated
-template <int BN, int ACT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<BN>::kThreads, 1)
-k_mm_pair(const __grid_constant__ MmParams p) {
+// Outputs 64 half .. 64 half + 63 of gated tile nt, one token per thread (token m0 + lane).
+__device__ __forceinline__ void put_gated(const MmParams& p, const float (&v)[64], uint8_t* stg, uint32_t* top, int nt,
+                                          int half, int q, int m0, bool ok, int lane) {
+  const int n0 = nt * 128 + 64 * half;
+  if (p.out != 2) {
+    put_values(p, v, stg, n0, m0, ok, lane);
+    return;
+  }
+  // a block is the 128 outputs of a token in this tile: its largest value from both halves
+  uint32_t a = 0;
+#pragma unroll
+  for (int i = 0; i < 64; ++i)
+    if (n0 + i < p.N) a = max(a, abs_bits(v[i]));
+  top[128 * half + 32 * q + lane] = a;
+  asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");
+  a = max(a, top[128 * (half ^ 1) + 32 * q + lane]);
+  asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");
+  const uint32_t byte = scale_byte(a);
+  const float is = inv_scale(byte);
+  uint32_t w[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) w[i] = e4m3x4(v[4 * i] * is, v[4 * i + 1] * is, v[4 * i + 2] * is, v[4 * i + 3] * is);
+  put_rows(w, stg, p.ocodes + static_cast<int64_t>(m0) * p.N + n0, p.N, p.N - n0, ok ? min(32, p.M - m0) : 0, lane);
+  if (ok && half == 0 && m0 + lane < p.M) p.osf[sf_offset(m0 + lane, nt, p.okatoms)] = static_cast<uint8_t>(byte);
+}
+
+// ACT: -1 plain, 0 SiLU-gated, 1 GELU-gated. SPLIT: K is shared by the 2 or 4 pairs of a cluster.
+template <int BN, int ACT, bool SPLIT>
+__global__ void __launch_bounds__(Pair<BN>::kThreads, 1) k_mm_pair(const __grid_constant__ MmParams p) {
   using C = Pair<BN>;
   constexpr bool GATED = ACT >= 0;
   constexpr int kBN = GATED ? BN / 2 : BN;                           // output columns of a tile
-  static_assert(!GATED || BN == 256, "an 8-bit block is the 128 outputs of a gated tile");
+  static_assert(!GATED || (BN == 256 && !SPLIT), "an 8-bit block is the 128 outputs of a gated tile");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(align_up(reinterpret_cast<uintptr_t>(smem_raw), 1024));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem);                // used in the first CTA
@@ -140,10 +168,13 @@ k_mm_pair(const __grid_constant__ MmParams p) {
   uint32_t* top = reinterpret_cast<uint32_t*>(smem + C::kTopOff);
 
   const int warp = warp_index(), lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
+  const uint32_t crank = cluster_ctarank(), rank = crank & 1u, lead = crank & ~1u;
+  const int splits = SPLIT ? p.splits : 1, split = static_cast<int>(crank >> 1);
+  const uint16_t both = static_cast<uint16_t>(3u << lead);           // the pair's CTAs in the cluster
   const int MT = static_cast<int>(cdiv(p.M, 256)), NT = static_cast<int>(cdiv(p.N, kBN)), T = MT * NT;
   const int KT = static_cast<int>(cdiv(p.K, kBlk));
-  const int first = static_cast<int>(blockIdx.x >> 1), step = static_cast<int>(gridDim.x >> 1);
+  const int kt0 = SPLIT ? KT * split / splits : 0, kt1 = SPLIT ? KT * (split + 1) / splits : KT;
+  const int first = static_cast<int>(blockIdx.x) / (2 * splits), step = static_cast<int>(gridDim.x) / (2 * splits);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
@@ -171,7 +202,7 @@ k_mm_pair(const __grid_constant__ MmParams p) {
     const CUtensorMap* map = tokens ? &p.tmap_x : &p.tmap_w[w];
     const uint32_t ring0 = smem_u32(ring) + (tokens ? 0 : C::kATile);
     const uint32_t sf0 = smem_u32(sfring) + (tokens ? 0 : 512);
-    const uint32_t bar0 = mapa_shared(smem_u32(&full[0]), 0), mine0 = smem_u32(&full[0]);
+    const uint32_t bar0 = mapa_shared(smem_u32(&full[0]), lead), mine0 = smem_u32(&full[0]);
     const uint32_t expect = tokens && rank == 0 ? one : 0u;
     uint32_t off = 0, st = ring0, sf = sf0;
     int s = 0;
@@ -187,12 +218,12 @@ k_mm_pair(const __grid_constant__ MmParams p) {
       // scale atoms by row group; a group past the last (its results are not stored) takes the last
       const int xa = min(m0 / 128, xb) * ka, wa0 = (GATED ? nt : nt * BN / 128) * ka,
                 wa1 = (GATED ? nt : min(nt * BN / 128 + 1, nb)) * ka;
-      for (int kt = 0; kt < KT; ++kt, ++it) {
+      for (int kt = kt0; kt < kt1; ++kt, ++it) {
         if (it >= C::kStages && !mbar_wait(&empty[s], ph, p.err, KQ_DEV_ERR_TIMEOUT_EMPTY)) {
           ok = false;
           break;
         }
-        const bool atom = (kt & 3) == 0;
+        const bool atom = (kt & 3) == 0 || (SPLIT && kt == kt0);
         expect_tx_if(expect, mine0 + off, 2 * (C::kStageBytes + (atom ? C::kSfBytes : 0u)));
         tma_load_pair_if(one, st, map, kt * kBlk, y, bar0 + off);
         if (atom) {
@@ -238,14 +269,14 @@ k_mm_pair(const __grid_constant__ MmParams p) {
           shift = static_cast<uint32_t>(nt * BN % 128) / 32u;
         }
         uint32_t acc = 0;
-        for (int kt = 0; kt < KT; ++kt) {
+        for (int kt = kt0; kt < kt1; ++kt) {
           if (!mbar_wait(&full[s], ph, p.err, KQ_DEV_ERR_TIMEOUT_FULL)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint32_t id = static_cast<uint32_t>(kt) & 3u;
-          if (id == 0) {
+          if (id == 0 || (SPLIT && kt == kt0)) {
             set = set + 1 == C::kSets ? 0 : set + 1;
             f = tmem + C::kSfCol + C::kSfSet * set;
             scale_cp_if<true>(one, f, sd);
@@ -258,29 +289,29 @@ k_mm_pair(const __grid_constant__ MmParams p) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             mma_mxf8_if<true>(one, d, ad0 + so + 2 * kk, bd0 + so + 2 * kk, idesc, fa, fa + 4 + shift, kk == 0 ? acc : 1u);
-          commit_if<true>(one, bar);
+          commit_if<true>(one, bar, both);
           acc = 1;
           so += C::kStageBytes >> 4;
           sd += C::kSfBytes >> 4;
           bar += 8;
           if (++s == C::kStages) { s = 0; ph ^= 1u; so = 0; sd = sd0; bar = smem_u32(empty); }
         }
-        commit_if<true>(one, smem_u32(&acc_full[buf]));
+        commit_if<true>(one, smem_u32(&acc_full[buf]), both);
       }
     }
   } else {
     grid_dep_wait();
     const int q = warp & 3, half = (warp - 2) >> 2;
     uint8_t* stg = smem + C::kStgOff + static_cast<uint32_t>(warp - 2) * C::kStgBytes;
-    const uint32_t free0 = mapa_shared(smem_u32(&acc_free[0]), 0);
+    const uint32_t free0 = mapa_shared(smem_u32(&acc_free[0]), lead);
     if (GATED && p.out == 2 && blockIdx.x == 0 && threadIdx.x == 64) *p.oerr = 0u;
     // Each warp of both CTAs frees an accumulator when it has read its columns (16 arrivals). Shared
     // columns are the second half's of accumulator 0 and the first half's of 1: their owner frees
     // the other accumulator after reading them, and its own after reading the rest; the first
     // half's share of accumulator 1's first turn is free from the start.
-    if (C::kShared && half == 0 && lane == 0) mbar_arrive_cluster(free0 + 8);
+    if (!SPLIT && C::kShared && half == 0 && lane == 0) mbar_arrive_cluster(free0 + 8);
     int local = 0;
-    for (int tile = first; tile < T; tile += step, ++local) {
+    for (int tile = SPLIT ? T : first; tile < T; tile += step, ++local) {
       int mt, nt;
       pair_tile(tile, MT, NT, mt, nt);
       const int m0 = mt * 256 + 128 * static_cast<int>(rank) + 32 * q;
@@ -327,7 +358,6 @@ k_mm_pair(const __grid_constant__ MmParams p) {
           for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i >> 5][i & 31]);
         }
         if (owner) release(buf ^ 1);
-        uint32_t a = 0;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t r[32];
@@ -340,27 +370,60 @@ k_mm_pair(const __grid_constant__ MmParams p) {
             v[32 * c + i] = gate_act<ACT>(buf == 0 ? o : f) * (buf == 0 ? f : o);
           }
         }
-        const int n0 = nt * 128 + 64 * half;
-        if (p.out != 2) {
-          put_values(p, v, stg, n0, m0, ok, lane);
-        } else {
-          // a block is the 128 outputs of a token in this tile: its largest value from both halves
+        put_gated(p, v, stg, top, nt, half, q, m0, ok, lane);
+      }
+    }
+  }
+  if (SPLIT) {
+    // The rows of lane quadrant q are finished by split q splits / 4 (2 or 4 splits): every split
+    // stores its partial sums of them over that CTA's ring, as [split][quadrant][4 columns][row],
+    // and its eight warps add them, 32 columns at a time, in the order of the splits.
+    const bool epi = warp >= 2 && warp < 10;
+    const int q = warp & 3, nq = 4 / splits;
+    bool ok = true;
+    if (epi) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[0], 0, p.err, KQ_DEV_ERR_TIMEOUT_ACC));
+      tc_fence_after();
+    }
+    __syncwarp();
+    cluster_sync();                                                  // every CTA's ring has been consumed
+    if (epi) {
+      const int dest = q / nq, half = (warp - 2) >> 2;
+      const uint32_t at = mapa_shared(smem_u32(ring), 2u * static_cast<uint32_t>(dest) + rank) +
+                          512u * static_cast<uint32_t>((split * nq + q - dest * nq) * (BN / 4)) +
+                          16u * static_cast<uint32_t>(lane);
+#pragma unroll 1
+      for (int c = BN / 2 * half; c < BN / 2 * (half + 1); c += 32) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(32 * q) << 16) + c, r);
+        tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 64; ++i)
-            if (n0 + i < p.N) a = max(a, abs_bits(v[i]));
-          top[128 * half + 32 * q + lane] = a;
-          asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");
-          a = max(a, top[128 * (half ^ 1) + 32 * q + lane]);
-          asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");
-          const uint32_t byte = scale_byte(a);
-          const float is = inv_scale(byte);
-          uint32_t w[16];
+        for (int j = 0; j < 8; ++j)
+          st_shared_cluster_v4(at + 512u * static_cast<uint32_t>(c / 4 + j), r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+      }
+    }
+    __syncwarp();
+    cluster_sync();
+    if (epi) {
+      const float4* part = reinterpret_cast<const float4*>(ring) + lane;
+      int mt, nt;
+      pair_tile(first, MT, NT, mt, nt);
+      uint8_t* stg = smem + C::kStgOff + static_cast<uint32_t>(warp - 2) * C::kStgBytes;
+#pragma unroll 1
+      for (int u = warp - 2; u < nq * (BN / 32); u += 8) {
+        const int qi = u % nq, c = u / nq * 32;
+        float v[32];
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            w[i] = e4m3x4(v[4 * i] * is, v[4 * i + 1] * is, v[4 * i + 2] * is, v[4 * i + 3] * is);
-          put_rows(w, stg, p.ocodes + static_cast<int64_t>(m0) * p.N + n0, p.N, p.N - n0, ok ? min(32, p.M - m0) : 0, lane);
-          if (ok && half == 0 && m0 + lane < p.M) p.osf[sf_offset(m0 + lane, nt, p.okatoms)] = static_cast<uint8_t>(byte);
+        for (int j = 0; j < 8; ++j) {
+          float4 t = part[(qi * (BN / 4) + c / 4 + j) * 32];
+          for (int s = 1; s < splits; ++s) {
+            const float4 w = part[((s * nq + qi) * (BN / 4) + c / 4 + j) * 32];
+            t.x += w.x; t.y += w.y; t.z += w.z; t.w += w.w;
+          }
+          v[4 * j] = t.x; v[4 * j + 1] = t.y; v[4 * j + 2] = t.z; v[4 * j + 3] = t.w;
         }
+        const int m0 = mt * 256 + 128 * static_cast<int>(rank) + 32 * (split * nq + qi);
+        if (nt * BN + c < p.N) put_values(p, v, stg, nt * BN + c, m0, ok, lane);
       }
     }
   }
@@ -373,46 +436,100 @@ k_mm_pair(const __grid_constant__ MmParams p) {
   }
 }
 
-template <int BN, int ACT>
+template <int BN, int ACT, bool SPLIT>
+cudaLaunchConfig_t pair_config(int64_t clusters, int splits, cudaLaunchAttribute (&attr)[2], cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * splits * clusters));
+  cfg.blockDim = dim3(Pair<BN>::kThreads);
+  cfg.dynamicSmemBytes = Pair<BN>::kSmem;
+  cfg.stream = st;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(2 * splits);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cfg;
+}
+
+template <int BN, int ACT, bool SPLIT>
 cudaError_t launch_pair_kernel(const MmParams& p, int sms, cudaStream_t st) {
-  using C = Pair<BN>;
-  auto fn = k_mm_pair<BN, ACT>;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem));
+  auto fn = k_mm_pair<BN, ACT, SPLIT>;
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(Pair<BN>::kSmem));
   if (e != cudaSuccess) return e;
   const int64_t tiles = cdiv(p.M, 256) * cdiv(p.N, ACT >= 0 ? BN / 2 : BN);
-  const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
-  cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  const int64_t clusters = SPLIT || tiles < sms / 2 ? tiles : sms / 2;
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = pair_config<BN, ACT, SPLIT>(clusters, SPLIT ? p.splits : 1, attr, st);
   return cudaLaunchKernelEx(&cfg, fn, p);
+}
+
+// Clusters of `splits` pairs that the device holds at once, one CTA per SM (a cluster stays within
+// a GPC: 33 of 4 CTAs and 15 of 8 on 148 SMs). Asked once per device.
+template <int BN>
+int64_t max_pair_clusters(int splits, int device) {
+  static std::atomic<int> known[kMaxDevices][2];
+  if (device >= kMaxDevices) return 0;
+  std::atomic<int>& k = known[device][splits / 4];
+  int n = k.load(std::memory_order_relaxed);
+  if (n > 0) return n - 1;
+  auto fn = k_mm_pair<BN, -1, true>;
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = pair_config<BN, -1, true>(1, splits, attr, nullptr);
+  cfg.numAttrs = 1;
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(Pair<BN>::kSmem)) !=
+          cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  k.store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
+// Keeps in `best` the shape that takes the least time: ns per k-tile and per tile of a pair as
+// measured with all SMs busy. Alone on its SMs a k-tile takes three quarters of that, which is what a
+// split saves of each, and the exchange 4.4 us (200 x 12288 -> 512: 17.0 us in one piece, 10.5 in
+// four; 128 x 4096 -> 4096: 8.6 and, in two, 10.5).
+template <int BN>
+void consider(int64_t tiles, int64_t kt, bool split, int64_t per_kt, int64_t per_tile, const Device& d, PairShape* best,
+              int64_t* cost) {
+  const int64_t plain = cdiv(tiles, d.sms / 2) * (per_kt * kt + per_tile);
+  if (plain < *cost) { *cost = plain; *best = {BN, 1}; }
+  for (int s = 2; split && s <= 4; s += 2) {
+    if (kt < 2 * s || tiles * s > d.sms / 2) continue;
+    const int64_t c = plain - (kt - cdiv(kt, s)) * per_kt * 3 / 4 + 4400;
+    if (c < *cost && tiles <= max_pair_clusters<BN>(s, d.device)) { *cost = c; *best = {BN, s}; }
+  }
 }
 
 }  // namespace
 
-int pair_cols(int M, int N, int K, bool gated, int sms) {
-  if (M <= kRowsMaxM) return 0;
-  if (gated) return 256;
-  // ns of a pair's share of the tiles: per k-tile and per tile, as measured
-  const int64_t kt = cdiv(K, kBlk), mt = cdiv(M, 256), pairs = sms / 2;
-  const int64_t c256 = cdiv(mt * cdiv(N, 256), pairs) * (340 * kt + 900);
-  const int64_t c192 = cdiv(mt * cdiv(N, 192), pairs) * (265 * kt + 550);
-  const int64_t c128 = cdiv(mt * cdiv(N, 128), pairs) * (200 * kt + 450);
-  return c128 < c192 && c128 < c256 ? 128 : c192 < c256 ? 192 : 256;
+PairShape pair_shape(int M, int N, int K, bool gated, const Device& d) {
+  PairShape best = {0, 1};
+  if (M <= kRowsMaxM) return best;
+  const int64_t kt = cdiv(K, kBlk), mt = cdiv(M, 256);
+  int64_t cost = INT64_MAX;
+  consider<256>(mt * cdiv(N, gated ? 128 : 256), kt, !gated, 340, 900, d, &best, &cost);
+  if (gated) return best;
+  consider<192>(mt * cdiv(N, 192), kt, true, 265, 550, d, &best, &cost);
+  consider<128>(mt * cdiv(N, 128), kt, true, 200, 450, d, &best, &cost);
+  return best;
+}
+
+template <int BN>
+static cudaError_t launch_plain(const MmParams& p, int sms, cudaStream_t st) {
+  return p.splits > 1 ? launch_pair_kernel<BN, -1, true>(p, sms, st) : launch_pair_kernel<BN, -1, false>(p, sms, st);
 }
 
 cudaError_t launch_pair(const MmParams& p, bool gated, int sms, cudaStream_t st) {
-  if (gated) return p.act == 0 ? launch_pair_kernel<256, 0>(p, sms, st) : launch_pair_kernel<256, 1>(p, sms, st);
+  if (gated) return p.act == 0 ? launch_pair_kernel<256, 0, false>(p, sms, st) : launch_pair_kernel<256, 1, false>(p, sms, st);
   switch (p.pairs) {
-    case 256: return launch_pair_kernel<256, -1>(p, sms, st);
-    case 192: return launch_pair_kernel<192, -1>(p, sms, st);
-    default: return launch_pair_kernel<128, -1>(p, sms, st);
+    case 256: return launch_plain<256>(p, sms, st);
+    case 192: return launch_plain<192>(p, sms, st);
+    default: return launch_plain<128>(p, sms, st);
   }
 }
 

@@ -39,7 +39,6 @@ namespace fp8 {
 namespace {
 
 constexpr int kMaxSplits = 8;
-constexpr int kMaxDevices = 64;
 
 template <int BT, bool GATED, bool FUSED>
 struct Rows {

@@ -76,15 +76,15 @@ __device__ __forceinline__ void scale_cp_if(uint32_t on, uint32_t taddr, uint64_
     asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}"
                  ::"r"(taddr), "l"(sdesc), "r"(on) : "memory");
 }
-// Arrive on a barrier (PAIR: on the one at this address in both CTAs) when the tcgen05 work that
-// the electing lane issued so far is done.
+// Arrive on a barrier (PAIR: on the one at this address in the cluster's CTAs `ctas`, a bit each)
+// when the tcgen05 work that the electing lane issued so far is done.
 template <bool PAIR>
-__device__ __forceinline__ void commit_if(uint32_t on, uint32_t bar) {
+__device__ __forceinline__ void commit_if(uint32_t on, uint32_t bar, uint16_t ctas = 0) {
   if (PAIR)
     asm volatile(
         "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
         "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}"
-        ::"r"(bar), "h"(static_cast<uint16_t>(3)), "r"(on) : "memory");
+        ::"r"(bar), "h"(ctas), "r"(on) : "memory");
   else
     asm volatile(
         "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
