@@ -426,7 +426,7 @@ kq_status kq_fp8_gated_act(const kq_fp8_desc *desc, const void *weights, void *a
 
 /* The layer on bf16 activations: the result of kq_fp8_quantize_act followed by kq_fp8_gemm. `act`
  * is scratch; whether the encoded activations are in it afterwards is not specified (for few
- * tokens the product's kernel encodes them on the way in). */
+ * tokens the product's kernel encodes them on the way in). Y may lie on X. */
 kq_status kq_fp8_linear(const kq_fp8_desc *desc, const void *weights, const void *X_bf16, int64_t ldx,
                         int32_t M, void *Y, int64_t ldy, int32_t out_dtype, void *act,
                         size_t act_bytes, kq_stream_t stream);
@@ -434,7 +434,7 @@ kq_status kq_fp8_linear(const kq_fp8_desc *desc, const void *weights, const void
 /* A feed-forward block, Y = (act(y Wgate) * (y Wup)) Wdown: kq_fp8_rmsnorm_act (gamma null:
  * kq_fp8_quantize_act, and no residual), kq_fp8_gated_act with `gated`, kq_fp8_gemm with
  * `down` (not gated, down->K == gated->N). ws: kq_fp8_ffn_bytes bytes (0 for invalid
- * arguments); it starts with the workspace kq_fp8_last_device_error takes. */
+ * arguments); it starts with the workspace kq_fp8_last_device_error takes. Y may lie on X. */
 size_t kq_fp8_ffn_bytes(const kq_fp8_desc *gated, const kq_fp8_desc *down, int32_t M);
 kq_status kq_fp8_ffn(const kq_fp8_desc *gated, const void *gated_weights, const kq_fp8_desc *down,
                      const void *down_weights, const void *X_bf16, int64_t ldx, void *residual,

@@ -490,3 +490,104 @@ def test_repacked_weights_are_read_at_once(cuda_device):
             kq.fp8_linear(L, w, X, Y2, act)
             torch.cuda.synchronize()
             assert torch.equal(Y, y) and torch.equal(Y2, y)
+
+
+@pytest.mark.parametrize("M", [1, 7, 40, 90])
+def test_output_on_the_input(cuda_device, M):
+    """Y in X's own buffer, and Y as other columns of the tensor that X is a part of."""
+    import torch
+    import w4a4_post_quantization_token_b200 as kq
+    K = N = 512
+    L = kq.Fp8Layer(K, N)
+    w, _ = packed(kq, L, weight(K, N, 1))
+    X = tokens(M, K, 3).cuda()
+    act = buf(kq.fp8_act_bytes(K, M))
+    want = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    kq.fp8_linear(L, w, X, want, act, kq.OUT_BF16)
+    inplace = X.clone()
+    kq.fp8_linear(L, w, inplace, inplace, act, kq.OUT_BF16)
+    both = torch.cat([X, torch.zeros_like(X)], 1)
+    kq.fp8_linear(L, w, both[:, :K], both[:, K:], act, kq.OUT_BF16)
+    assert torch.equal(inplace, want) and torch.equal(both[:, K:], want) and torch.equal(both[:, :K], X)
+    G, gw, D, dw, *_ = make_ffn(kq, K, 544)
+    gamma = torch.rand(K, device="cuda")
+    ws = buf(kq.fp8_ffn_bytes(G, D, M))
+    kq.fp8_ffn(G, gw, D, dw, X, gamma, EPS, want, ws, kq.OUT_BF16)
+    kq.fp8_ffn(G, gw, D, dw, X, gamma, EPS, X, ws, kq.OUT_BF16)
+    assert torch.equal(X, want)
+
+
+@pytest.mark.parametrize("M", [2, 50, 130])
+def test_two_streams_at_once(cuda_device, M):
+    """Blocks on two streams, each with a workspace of its own, do not disturb each other."""
+    import torch
+    import w4a4_post_quantization_token_b200 as kq
+    K, N = 1024, 2048
+    G, gw, D, dw, *_ = make_ffn(kq, K, N)
+    gamma = torch.rand(K, device="cuda")
+    Xs = [tokens(M, K, 20 + i).cuda() for i in range(2)]
+    want = []
+    for X in Xs:
+        Y = torch.empty(M, K, device="cuda")
+        kq.fp8_ffn(G, gw, D, dw, X, gamma, EPS, Y, buf(kq.fp8_ffn_bytes(G, D, M)))
+        want.append(Y)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in Xs]
+    got = [torch.empty(20, M, K, device="cuda") for _ in Xs]
+    spaces = [buf(kq.fp8_ffn_bytes(G, D, M)) for _ in Xs]
+    torch.cuda.synchronize()
+    for k in range(20):
+        for i, X in enumerate(Xs):
+            kq.fp8_ffn(G, gw, D, dw, X, gamma, EPS, got[i][k], spaces[i], stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert kq.fp8_last_device_error(spaces[i]) == 0
+        assert all(torch.equal(got[i][k], want[i]) for k in range(20))
+
+
+def test_two_graphs_share_a_workspace(cuda_device):
+    """Two captured layers that use one workspace, replayed in turn on one stream."""
+    import torch
+    import w4a4_post_quantization_token_b200 as kq
+    cases = []
+    act = buf(max(kq.fp8_act_bytes(1024, 70), kq.fp8_act_bytes(2048, 5)))
+    for M, K, N in ((70, 1024, 512), (5, 2048, 256)):
+        L = kq.Fp8Layer(K, N)
+        w, _ = packed(kq, L, weight(K, N, K))
+        X, Y = tokens(M, K, M).cuda(), torch.empty(M, N, device="cuda")
+        kq.fp8_linear(L, w, X, Y, act)
+        torch.cuda.synchronize()
+        want = Y.clone()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            kq.fp8_linear(L, w, X, Y, act)
+        cases.append((g, Y, want, X, w))
+    for _ in range(5):
+        for g, Y, *_ in cases:
+            Y.zero_()
+            g.replay()
+        torch.cuda.synchronize()
+        for _, Y, want, *_ in cases:
+            assert torch.equal(Y, want)
+
+
+@pytest.mark.parametrize("M", [2, 200])
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_gate_far_from_zero(cuda_device, M, kind):
+    """Gates of +-1e4 and beyond: the activation is its limit (0 or the gate itself), never NaN."""
+    import torch
+    import w4a4_post_quantization_token_b200 as kq
+    K, N = 64, 128
+    X = torch.zeros(M, K, dtype=torch.bfloat16)
+    X[0::2, 0], X[1::2, 0], X[:, 1] = 1e4, -1e4, 2.0
+    W, Wu = torch.zeros(K, N, dtype=torch.bfloat16), torch.zeros(K, N, dtype=torch.bfloat16)
+    W[0] = 8.0
+    Wu[1] = 1.0
+    L = kq.Fp8Layer(K, N, gated=True, activation=kind)
+    w, (Wd, Wud) = packed(kq, L, W, Wu)
+    Y = torch.empty(M, N, device="cuda")
+    kq.fp8_linear(L, w, X.cuda(), Y, buf(kq.fp8_act_bytes(K, M)))
+    A = fp8.decode_rows(*fp8.encode_rows(_np(X)))
+    z, u = A @ Wd.T, A @ Wud.T
+    assert np.all(np.abs(z) > 7e4)
+    np.testing.assert_allclose(_np(Y), np.where(z > 0, z, 0) * u, rtol=2.0 ** -18, atol=1e-30)

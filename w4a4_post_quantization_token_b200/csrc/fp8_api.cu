@@ -38,6 +38,13 @@ kq_status check_act(const void* act, size_t bytes, int32_t K, int32_t M) {
   return bytes < fp8::ALayout::make(M, K).total ? KQ_ERR_WORKSPACE_TOO_SMALL : KQ_OK;
 }
 
+// Whether two matrices' address ranges meet (rows of `w` bytes, `pitch` bytes apart).
+bool meet(const void* a, int64_t pa, int64_t wa, const void* b, int64_t pb, int64_t wb, int32_t rows) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  const uintptr_t a1 = a0 + static_cast<uintptr_t>((rows - 1) * pa + wa), b1 = b0 + static_cast<uintptr_t>((rows - 1) * pb + wb);
+  return a0 < b1 && b0 < a1;
+}
+
 struct Norm {
   void* residual = nullptr;
   int64_t ldr = 0;
@@ -113,11 +120,14 @@ kq_status run_mm(const kq_fp8_desc* d, const void* weights, uint8_t* act, int32_
     p.oerr = reinterpret_cast<uint32_t*>(oact + O.err);
   }
   if (xb) {
-    // bf16 activations: few tokens are encoded by the product's own kernel
+    // bf16 activations: few tokens are encoded by the product's own kernel, unless its output may
+    // lie on them (other CTAs would still read)
     p.xb = xb;
     p.ldx = ldx;
+    const int64_t ye = out == 1 ? 2 : 4;
+    const bool apart = !meet(xb, ldx * 2, int64_t{2} * d->K, Y, ldy * ye, ye * d->N, M);
     cudaError_t e = cudaSuccess;
-    if (!p.pairs && fp8::try_rows_fused(p, d->gated != 0, dev, st, &e)) return e == cudaSuccess ? KQ_OK : KQ_ERR_CUDA;
+    if (!p.pairs && apart && fp8::try_rows_fused(p, d->gated != 0, dev, st, &e)) return e == cudaSuccess ? KQ_OK : KQ_ERR_CUDA;
     const kq_status s = run_rows(d->K, xb, ldx, nullptr, M, act, st);
     if (s != KQ_OK) return s;
     dependent = true;
