@@ -74,42 +74,55 @@ struct Rows {
   // A scale set is rewritten three atoms later, 9 k-tiles at least after its last use: those
   // MMAs have freed the stage that the new atom landed in.
   static_assert(kStages <= 9, "scale sets");
-  static_assert(kPartBytes <= kRingBytes, "exchange over the ring");
+  static_assert(kPartBytes + 2048 <= kRingBytes, "exchange and codes over the ring");
   // The CTAs of a cluster wait for one another, so that none may wait for TMEM columns which a
   // CTA of another cluster on its SM holds: columns for two.
   static_assert(kTmemCols <= 256, "two CTAs per SM");
 };
 
 // One thread's feature n0 + 32 q + lane of T tokens from `token`, `lim` of which exist. The four
-// epilogue warps call it together: a block of the 8-bit output is the CTA's 128 features of one
-// token, and its largest value is found across them (`top` [4][16]).
+// epilogue warps call it together. A block of the 8-bit output is the CTA's 128 features of one
+// token: its largest value is found across the warps (`top` [4][16]), the codes are put together
+// in `tile` [T][128] and written 16 to a store.
 template <int T, bool GATED>
 __device__ __forceinline__ void store(const MmParams& p, const float* v, int token, int lim, int n0, int q, int lane,
-                                      uint32_t* top) {
+                                      uint32_t* top, uint8_t* tile) {
   const int n = n0 + 32 * q + lane;
   if (GATED && p.out == 2) {
-    asm volatile("bar.sync 1, 128;" ::: "memory");          // the maxima of the last call were read
+    asm volatile("bar.sync 1, 128;" ::: "memory");          // the last call's maxima and codes were read
+    uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < T; ++j) {
-      const uint32_t m = __reduce_max_sync(0xffffffffu, n < p.N ? abs_bits(v[j]) : 0u);
-      if (lane == 0) top[q * 16 + j] = m;
+      const uint32_t mj = __reduce_max_sync(0xffffffffu, n < p.N ? abs_bits(v[j]) : 0u);
+      if (lane == j) m = mj;
+    }
+    if (lane < T) top[q * 16 + lane] = m;
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    if (lane < T) m = scale_byte(max(max(top[lane], top[16 + lane]), max(top[32 + lane], top[48 + lane])));
+    if (q == 0 && lane < T && lane < lim)
+      p.osf[sf_offset(static_cast<int64_t>(token) + lane, n0 / 128, p.okatoms)] = static_cast<uint8_t>(m);
+#pragma unroll
+    for (int j = 0; j < T; ++j) {
+      const float is = inv_scale(__shfl_sync(0xffffffffu, m, j));
+      tile[128 * j + 32 * q + lane] = static_cast<uint8_t>(e4m3x2(v[j] * is, 0.f));
     }
     asm volatile("bar.sync 1, 128;" ::: "memory");
-#pragma unroll
-    for (int j = 0; j < T; ++j) {
-      if (j >= lim) break;
-      const uint32_t byte = scale_byte(max(max(top[j], top[16 + j]), max(top[32 + j], top[48 + j])));
-      const int64_t t = static_cast<int64_t>(token) + j;
-      if (n < p.N) p.ocodes[t * p.N + n] = static_cast<uint8_t>(e4m3x2(v[j] * inv_scale(byte), 0.f));
-      if (q == 0 && lane == 0) p.osf[sf_offset(t, n0 / 128, p.okatoms)] = static_cast<uint8_t>(byte);
-    }
+    const int i = 32 * q + lane, j = i >> 3, c = 16 * (i & 7);       // 8 threads to a token
+    if (j < lim && j < T && n0 + c < p.N)
+      *reinterpret_cast<uint4*>(p.ocodes + (static_cast<int64_t>(token) + j) * p.N + n0 + c) =
+          *reinterpret_cast<const uint4*>(tile + 128 * j + c);
   } else if (n < p.N) {
+    const int64_t at = static_cast<int64_t>(token) * p.ldy + n;
+    if (p.out == 1) {
+      __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + at;
 #pragma unroll
-    for (int j = 0; j < T; ++j) {
-      if (j >= lim) break;
-      const int64_t at = (static_cast<int64_t>(token) + j) * p.ldy + n;
-      if (p.out == 1) static_cast<__nv_bfloat16*>(p.y)[at] = __float2bfloat16_rn(v[j]);
-      else static_cast<float*>(p.y)[at] = v[j];
+      for (int j = 0; j < T; ++j, y += p.ldy)
+        if (j < lim) *y = __float2bfloat16_rn(v[j]);
+    } else {
+      float* y = static_cast<float*>(p.y) + at;
+#pragma unroll
+      for (int j = 0; j < T; ++j, y += p.ldy)
+        if (j < lim) *y = v[j];
     }
   }
 }
@@ -152,8 +165,10 @@ __device__ __forceinline__ void encode_share(const MmParams& p, int tokens, int 
   }
 }
 
-template <int BT, bool GATED, bool FUSED>
-__global__ void __launch_bounds__(Rows<BT, GATED, FUSED>::kThreads) k_rows_mm(const __grid_constant__ MmParams p) {
+// ACT: -1 plain, 0 SiLU-gated, 1 GELU-gated
+template <int BT, int ACT, bool FUSED>
+__global__ void __launch_bounds__(Rows<BT, ACT >= 0, FUSED>::kThreads) k_rows_mm(const __grid_constant__ MmParams p) {
+  constexpr bool GATED = ACT >= 0;
   using C = Rows<BT, GATED, FUSED>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(align_up(reinterpret_cast<uintptr_t>(smem_raw), 1024));
@@ -283,6 +298,7 @@ __global__ void __launch_bounds__(Rows<BT, GATED, FUSED>::kThreads) k_rows_mm(co
   }
   const int q = warp & 3;                                  // TMEM lane quadrant
   const uint32_t tb = tmem + (static_cast<uint32_t>(32 * q) << 16);
+  uint8_t* tile = ring + (C::kOwnPart ? 0 : C::kPartBytes);             // the ring is read by then
   const bool epi = warp >= 2 && warp < 6;
   bool ok = true;
   if (epi || (FUSED && warp > 6)) {
@@ -335,19 +351,23 @@ __global__ void __launch_bounds__(Rows<BT, GATED, FUSED>::kThreads) k_rows_mm(co
     cluster_sync();
     if (epi) {
       const int qs = Q * rank / splits, qe = Q * (rank + 1) / splits;
-      for (int four = qs; four < qe; ++four) {
-        float v[C::kProducts][4] = {};
+      // up to four fours to a call of store, which the 8-bit output makes a meeting of the warps
+      constexpr int F = BT <= 16 ? 1 : 4;
+      for (int four = qs; four < qe; four += F) {
+        float v[C::kProducts][4 * F] = {};
         for (int s = 0; s < splits; ++s)
 #pragma unroll
-          for (int j = 0; j < C::kProducts; ++j) {
-            const float4 w = part[((s * C::kProducts + j) * cap + four - qs) * 128 + 32 * q + lane];
-            v[j][0] += w.x; v[j][1] += w.y; v[j][2] += w.z; v[j][3] += w.w;
-          }
+          for (int j = 0; j < C::kProducts; ++j)
+#pragma unroll
+            for (int f = 0; f < F; ++f) {
+              if (f > 0 && four + f >= qe) break;
+              const float4 w = part[((s * C::kProducts + j) * cap + four + f - qs) * 128 + 32 * q + lane];
+              v[j][4 * f] += w.x; v[j][4 * f + 1] += w.y; v[j][4 * f + 2] += w.z; v[j][4 * f + 3] += w.w;
+            }
         if (GATED)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            v[0][i] = (p.act == 0 ? gate_act<0>(v[0][i]) : gate_act<1>(v[0][i])) * v[C::kProducts - 1][i];
-        store<4, GATED>(p, v[0], 4 * four, ok ? min(4, tokens - 4 * four) : 0, n0, q, lane, top);
+          for (int i = 0; i < 4 * F; ++i) v[0][i] = gate_act<ACT>(v[0][i]) * v[C::kProducts - 1][i];
+        store<4 * F, GATED>(p, v[0], 4 * four, ok ? min(min(4 * F, 4 * (qe - four)), tokens - 4 * four) : 0, n0, q, lane, top, tile);
       }
     }
   } else if (epi) {
@@ -361,9 +381,9 @@ __global__ void __launch_bounds__(Rows<BT, GATED, FUSED>::kThreads) k_rows_mm(co
       for (int t = 0; t < 16; ++t) {
         v[t] = __uint_as_float(r[0][t]);
         if (GATED)
-          v[t] = (p.act == 0 ? gate_act<0>(v[t]) : gate_act<1>(v[t])) * __uint_as_float(r[C::kProducts - 1][t]);
+          v[t] = gate_act<ACT>(v[t]) * __uint_as_float(r[C::kProducts - 1][t]);
       }
-      store<16, GATED>(p, v, c, ok ? min(16, tokens - c) : 0, n0, q, lane, top);
+      store<16, GATED>(p, v, c, ok ? min(16, tokens - c) : 0, n0, q, lane, top, tile);
     }
   }
   tc_fence_before();
@@ -395,7 +415,7 @@ cudaLaunchConfig_t rows_config(const MmParams& p, int splits, cudaLaunchAttribut
 // Clusters of s CTAs of this kernel that the device holds at once (fewer than SMs / s, since a
 // cluster stays within a GPC: 15 of 8 CTAs on 148 SMs). Asked once per device, with the most
 // shared memory that the kernel takes.
-template <int BT, bool GATED, bool FUSED>
+template <int BT, int ACT, bool FUSED>
 int max_clusters(int s, int device) {
   static std::atomic<int> known[kMaxDevices][kMaxSplits + 1];
   if (device >= kMaxDevices) return 0;
@@ -403,12 +423,12 @@ int max_clusters(int s, int device) {
   if (n > 0) return n - 1;
   MmParams p = {};
   p.N = 128;
-  p.K = kBlk * s * (FUSED ? Rows<BT, GATED, FUSED>::kMaxShare : 1);
+  p.K = kBlk * s * (FUSED ? Rows<BT, ACT >= 0, FUSED>::kMaxShare : 1);
   cudaLaunchAttribute attr[2];
-  cudaLaunchConfig_t cfg = rows_config<BT, GATED, FUSED>(p, s, attr, nullptr);
+  cudaLaunchConfig_t cfg = rows_config<BT, ACT >= 0, FUSED>(p, s, attr, nullptr);
   cfg.attrs = attr + 1;
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, k_rows_mm<BT, GATED, FUSED>, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, k_rows_mm<BT, ACT, FUSED>, &cfg) != cudaSuccess) {
     cudaGetLastError();
     n = 0;
   }
@@ -418,39 +438,40 @@ int max_clusters(int s, int device) {
 
 // Splits of K for `tiles` tiles of `kt` k-tiles: the number that leaves a CTA the fewest k-tiles
 // while all CTAs run at once, one per SM. A split has to take off more than the exchange costs.
-template <int BT, bool GATED, bool FUSED>
+template <int BT, int ACT, bool FUSED>
 int rows_splits(int64_t tiles, int64_t kt, int sms, int device) {
   int best = 1;
   int64_t cost = cdiv(tiles, sms) * kt;
   for (int s = 2; s <= kMaxSplits && tiles * s <= sms && kt >= 2 * s; ++s) {
     const int64_t c = cdiv(kt, s) + 4;
-    if (c < cost && tiles <= max_clusters<BT, GATED, FUSED>(s, device)) { best = s; cost = c; }
+    if (c < cost && tiles <= max_clusters<BT, ACT, FUSED>(s, device)) { best = s; cost = c; }
   }
   return best;
 }
 
-template <int BT, bool GATED, bool FUSED>
+template <int BT, int ACT, bool FUSED>
 bool try_rows(const MmParams& p, const Device& d, cudaStream_t st, cudaError_t* e) {
-  using C = Rows<BT, GATED, FUSED>;
-  auto fn = k_rows_mm<BT, GATED, FUSED>;
+  using C = Rows<BT, ACT >= 0, FUSED>;
+  auto fn = k_rows_mm<BT, ACT, FUSED>;
   *e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                             static_cast<int>(C::smem(FUSED ? C::kMaxShare : 0)));
   if (*e != cudaSuccess) return true;
   const int64_t kt = cdiv(p.K, kBlk);
-  const int splits = rows_splits<BT, GATED, FUSED>(cdiv(p.N, 128), kt, d.sms, d.device);
-  // One round of encoding costs about what a kernel of its own adds behind this one's start (one
-  // token, 4096 -> 4096: 5.3 us for both together, 6.0 as two kernels; eight: 6.3 and 6.3), and
-  // saves a launch; more rounds cost more (32 tokens: 10.0 and 7.1).
-  if (FUSED && (cdiv(kt, splits) > C::kMaxShare || cdiv(kt, splits) * p.M > kEncRound)) return false;
+  const int splits = rows_splits<BT, ACT, FUSED>(cdiv(p.N, 128), kt, d.sms, d.device);
+  // Encoding on the way in adds 0.8 us to the product for 4 blocks of a CTA, 1.3 for 32, 1.7 for 64
+  // and 2.5 for 128 (512 -> 512, 1 to 32 tokens), a kernel of its own 1.6 and a launch, which costs
+  // the host more than 2 us: half a round of blocks at most.
+  if (FUSED && (cdiv(kt, splits) > C::kMaxShare || cdiv(kt, splits) * p.M > kEncRound / 2)) return false;
   cudaLaunchAttribute attr[2];
-  const cudaLaunchConfig_t cfg = rows_config<BT, GATED, FUSED>(p, splits, attr, st);
+  const cudaLaunchConfig_t cfg = rows_config<BT, ACT >= 0, FUSED>(p, splits, attr, st);
   *e = cudaLaunchKernelEx(&cfg, fn, p);
   return true;
 }
 
 template <int BT, bool FUSED>
 bool try_rows_g(const MmParams& p, bool gated, const Device& d, cudaStream_t st, cudaError_t* e) {
-  return gated ? try_rows<BT, true, FUSED>(p, d, st, e) : try_rows<BT, false, FUSED>(p, d, st, e);
+  if (!gated) return try_rows<BT, -1, FUSED>(p, d, st, e);
+  return p.act == 0 ? try_rows<BT, 0, FUSED>(p, d, st, e) : try_rows<BT, 1, FUSED>(p, d, st, e);
 }
 
 }  // namespace
