@@ -56,7 +56,9 @@ __device__ __forceinline__ void store32(void* p, bool wide, const uint32_t* u) {
 }
 
 // The plain quantizer: kRowsC chunks of 16 features (32 bytes) per thread, loaded together; 8
-// neighbouring threads share a scale; blockDim.x threads along a row, blockDim.y rows.
+// neighbouring threads share a scale; blockDim.x threads along a row, blockDim.y rows. Bound by HBM:
+// 3 bytes a feature, 8192 x 8192 in 31.6 us (6.4 TB/s, the copy rate; with 16-byte accesses
+// 40 us). Few tokens cost one load latency and a launch, 1.8 us for 1 x 4096.
 constexpr int kRowsC = 4;
 __global__ void __launch_bounds__(256) k_quant(const __grid_constant__ NormParams p, bool wide) {
   enter(p);
@@ -103,7 +105,10 @@ __global__ void __launch_bounds__(256) k_quant(const __grid_constant__ NormParam
 //   h = x + residual in fp32, rounded to the residual's type and kept there;
 //   r = 1 / sqrt(mean(h^2) + eps), the sum and the root in float64, rounded once to fp32;
 //   y = (h r) gamma, two fp32 products; then the block's scale and codes from y.
-// The float64 sum makes r, and so every code, independent of the summation order.
+// The float64 sum makes r, and so every code, independent of the summation order. Bound by HBM: the
+// row stays in registers between the sum and the codes, so that x and the residual are read once:
+// 8192 x 8192 with a bf16 residual in 72.7 us (7 bytes a feature, 6.46 TB/s, the copy rate; 106 us
+// when a chunk's residual was stored before the next chunk's load), 1 x 4096 in 2.4 us.
 template <int C, int RES>
 __global__ void __launch_bounds__(512) k_norm(const __grid_constant__ NormParams p) {
   __shared__ double part[16];
@@ -262,7 +267,7 @@ __global__ void k_act_scales(uint8_t* canon, int kb, int64_t count, uint8_t* sf,
 
 // The values that codes stand for: two chunks of 32 codes per thread (K is a multiple of 32, so a
 // chunk lies in one block), both loaded first. `wide`: 32-byte accesses to the codes (1), the
-// values (2).
+// values (2). Bound by HBM: 8192 x 8192 to bf16 in 31.2 us (6.45 TB/s).
 template <bool BF16>
 __global__ void __launch_bounds__(256) k_act_values(const uint8_t* codes, const uint8_t* sf, int K, int64_t chunks,
                                                     int64_t ka, uint8_t* out, int wide) {
