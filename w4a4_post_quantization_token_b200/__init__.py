@@ -403,11 +403,31 @@ class Fp8Layer:
     def __init__(self, K: int, N: int, gated: bool = False, activation: str = "silu"):
         self.K, self.N, self.gated, self.activation = int(K), int(N), bool(gated), activation
         self._desc = _Fp8Desc(K=self.K, N=self.N, gated=int(self.gated), activation=_ACTIVATION[activation])
+        self._ref = ctypes.byref(self._desc)
         self._weights_bytes = fp8_weights_bytes(self)
 
     @property
     def desc(self):
-        return ctypes.byref(self._desc)
+        return self._ref
+
+
+class _Names:
+    """What the 8-bit calls use of torch, looked up once: a call for one token takes a few
+    microseconds on the host, and each lookup on its way counts."""
+
+    def __init__(self):
+        import torch
+        self.u8, self.f32 = torch.uint8, torch.float32
+        self.bf16 = (torch.bfloat16,)
+        self.out = {OUT_F32: (torch.float32,), OUT_BF16: (torch.bfloat16,)}
+        self.flag = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
+        self.raw_stream, self.device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        self.guard = torch.cuda.device
+
+
+@functools.lru_cache(maxsize=None)
+def _names() -> _Names:
+    return _Names()
 
 
 def _rows(t, dtypes, rows: int | None, width: int, name: str) -> int:
@@ -427,7 +447,7 @@ def _rows(t, dtypes, rows: int | None, width: int, name: str) -> int:
 
 
 def _flat(t, dtype, numel: int, name: str):
-    """Checks a contiguous tensor of at least numel elements (its device: _fp8_run)."""
+    """Checks a contiguous tensor of at least numel elements (its device: _fp8_call)."""
     if t is None:
         raise ValueError(f"{name} is required")
     if t.dtype is not dtype:
@@ -439,31 +459,28 @@ def _flat(t, dtype, numel: int, name: str):
     return t
 
 
-def _fp8_run(fn, where: str, stream, tensors, *args) -> None:
+def _fp8_call(fn, where: str, stream, tensors, args) -> None:
     """Calls fn(*args, stream) on the device of `tensors`, which must all be on one CUDA device,
     and on `stream` or that device's current stream."""
-    import torch
-    dev = -1
+    names = _names()
+    dev = tensors[0].get_device()
     for t in tensors:
-        if t is not None:
-            d = t.get_device()
-            if d < 0:
-                raise ValueError(f"{where}: every tensor must be a CUDA tensor")
-            if d != dev and dev >= 0:
-                raise ValueError(f"{where}: tensors are on different devices")
-            dev = d
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{where}: tensors are on different devices")
+    if dev < 0:
+        raise ValueError(f"{where}: every tensor must be a CUDA tensor")
     if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(dev)
+        raw = names.raw_stream(dev)
     elif stream.device_index != dev:
         raise ValueError(f"{where}: the stream is of another device than the tensors")
     else:
         raw = stream.cuda_stream
-    if torch._C._cuda_getDevice() == dev:
+    if names.device() == dev:
         status = fn(*args, raw)
     else:
-        with torch.cuda.device(dev):
+        with names.guard(dev):
             status = fn(*args, raw)
-    if status != 0:
+    if status:
         raise KQError(status, where)
 
 
@@ -486,10 +503,9 @@ def _fp8_pair(layer: Fp8Layer, up, name: str) -> None:
 
 
 def _fp8_weights(layer: Fp8Layer, weights):
-    import torch
-    if layer._weights_bytes == 0:
+    if not layer._weights_bytes:
         raise ValueError(f"unsupported 8-bit layer K={layer.K} N={layer.N}")
-    return _flat(weights, torch.uint8, layer._weights_bytes, "weights")
+    return _flat(weights, _names().u8, layer._weights_bytes, "weights")
 
 
 def _e4m3(t, numel: int, name: str):
@@ -506,8 +522,8 @@ def fp8_prepare_weights(layer: Fp8Layer, W, weights, W_up=None, stream=None) -> 
     _fp8_weights(layer, weights)
     for t, name in ((W, "W"), (W_up, "W_up"))[:1 + layer.gated]:
         _flat(t, torch.bfloat16, layer.K * layer.N, name)
-    _fp8_run(lib.kq_fp8_prepare_weights, "kq_fp8_prepare_weights", stream, (W, W_up, weights), layer.desc, _ptr(W),
-             _ptr(W_up), _ptr(weights))
+    _fp8_call(lib.kq_fp8_prepare_weights, "kq_fp8_prepare_weights", stream, (W, W_up, weights),
+              (layer.desc, _ptr(W), _ptr(W_up), _ptr(weights)))
 
 
 def _fp8_parts(layer: Fp8Layer, codes, scales, up_codes, up_scales, optional: bool):
@@ -528,53 +544,50 @@ def fp8_weights_pack(layer: Fp8Layer, codes, scales, weights, up_codes=None, up_
     [ceil(N / 128), ceil(K / 128)] (exponent + 127); gated layers take the up_ pair too."""
     _fp8_weights(layer, weights)
     parts = _fp8_parts(layer, codes, scales, up_codes, up_scales, optional=False)
-    _fp8_run(lib.kq_fp8_weights_pack, "kq_fp8_weights_pack", stream, (weights, *parts), layer.desc, *map(_ptr,
-             parts), _ptr(weights))
+    _fp8_call(lib.kq_fp8_weights_pack, "kq_fp8_weights_pack", stream, (weights, *parts),
+              (layer.desc, *map(_ptr, parts), _ptr(weights)))
 
 
 def fp8_weights_unpack(layer: Fp8Layer, weights, codes=None, scales=None, up_codes=None, up_scales=None,
                    stream=None) -> None:
     _fp8_weights(layer, weights)
     parts = _fp8_parts(layer, codes, scales, up_codes, up_scales, optional=True)
-    _fp8_run(lib.kq_fp8_weights_unpack, "kq_fp8_weights_unpack", stream, (weights, *parts), layer.desc,
-             _ptr(weights), *map(_ptr, parts))
+    _fp8_call(lib.kq_fp8_weights_unpack, "kq_fp8_weights_unpack", stream, (weights, *parts),
+              (layer.desc, _ptr(weights), *map(_ptr, parts)))
 
 
 def _fp8_act(act, K: int, M: int, name: str = "act"):
-    import torch
-    return _flat(act, torch.uint8, fp8_act_bytes(K, M), name)
+    return _flat(act, _names().u8, fp8_act_bytes(K, M), name)
 
 
 def fp8_quantize_act(X, act, stream=None) -> None:
     """Quantize X (bf16 [M, K], rows may be a pitch apart) into an activation workspace."""
-    import torch
     M, K = X.shape
-    ldx = _rows(X, (torch.bfloat16,), None, K, "X")
+    ldx = _rows(X, _names().bf16, None, K, "X")
     _fp8_act(act, K, M)
-    _fp8_run(lib.kq_fp8_quantize_act, "kq_fp8_quantize_act", stream, (X, act), K, _ptr(X), ldx, M, _ptr(act),
-             act.numel())
+    _fp8_call(lib.kq_fp8_quantize_act, "kq_fp8_quantize_act", stream, (X, act),
+              (K, X.data_ptr(), ldx, M, act.data_ptr(), act.numel()))
 
 
 def _fp8_norm(gamma, residual, M: int, K: int):
-    """(residual pitch, residual dtype) after the checks."""
-    import torch
-    _flat(gamma, torch.float32, K, "gamma")
+    """(residual address, pitch, dtype) after the checks."""
+    names = _names()
+    _flat(gamma, names.f32, K, "gamma")
     if residual is None:
-        return 0, OUT_F32
-    ldr = _rows(residual, (torch.bfloat16, torch.float32), M, K, "residual")
-    return ldr, OUT_BF16 if residual.dtype == torch.bfloat16 else OUT_F32
+        return None, 0, OUT_F32
+    ldr = _rows(residual, names.flag, M, K, "residual")
+    return residual.data_ptr(), ldr, names.flag[residual.dtype]
 
 
 def fp8_rmsnorm_act(X, gamma, eps: float, act, residual=None, stream=None) -> None:
     """Root-mean-square norm of X + residual times gamma, quantized into act; residual (bf16 or
     fp32 [M, K]) is replaced by the sum."""
-    import torch
     M, K = X.shape
-    ldx = _rows(X, (torch.bfloat16,), None, K, "X")
-    ldr, rdt = _fp8_norm(gamma, residual, M, K)
+    ldx = _rows(X, _names().bf16, None, K, "X")
+    res, ldr, rdt = _fp8_norm(gamma, residual, M, K)
     _fp8_act(act, K, M)
-    _fp8_run(lib.kq_fp8_rmsnorm_act, "kq_fp8_rmsnorm_act", stream, (X, gamma, residual, act), K, _ptr(X), ldx,
-             _ptr(residual), ldr, rdt, _ptr(gamma), float(eps), M, _ptr(act), act.numel())
+    _fp8_call(lib.kq_fp8_rmsnorm_act, "kq_fp8_rmsnorm_act", stream, (X, gamma, act, residual),
+              (K, X.data_ptr(), ldx, res, ldr, rdt, gamma.data_ptr(), eps, M, act.data_ptr(), act.numel()))
 
 
 def fp8_act_pack(K: int, codes, scales, M: int, act, stream=None) -> None:
@@ -582,30 +595,32 @@ def fp8_act_pack(K: int, codes, scales, M: int, act, stream=None) -> None:
     codes = _e4m3(codes, M * K, "codes")
     _flat(scales, torch.uint8, M * -(-K // 128), "scales")
     _fp8_act(act, K, M)
-    _fp8_run(lib.kq_fp8_act_pack, "kq_fp8_act_pack", stream, (codes, scales, act), int(K), _ptr(codes),
-             _ptr(scales), int(M), _ptr(act), act.numel())
+    _fp8_call(lib.kq_fp8_act_pack, "kq_fp8_act_pack", stream, (codes, scales, act),
+              (int(K), _ptr(codes), _ptr(scales), int(M), _ptr(act), act.numel()))
 
 
 def fp8_act_unpack(K: int, act, M: int, codes=None, scales=None, values=None, stream=None) -> None:
     """Read an activation workspace: codes [M, K], scales uint8 [M, ceil(K / 128)], values (bf16
     or fp32 [M, K]) = code * 2^(scale - 127); parts that are None are skipped."""
-    import torch
+    names = _names()
     _fp8_act(act, K, M)
     vdt = OUT_F32
     if codes is not None:
         codes = _e4m3(codes, M * K, "codes")
     if scales is not None:
-        _flat(scales, torch.uint8, M * -(-K // 128), "scales")
+        _flat(scales, names.u8, M * -(-K // 128), "scales")
     if values is not None:
-        vdt = OUT_BF16 if values.dtype == torch.bfloat16 else OUT_F32
-        _flat(values, torch.bfloat16 if vdt == OUT_BF16 else torch.float32, M * K, "values")
-    _fp8_run(lib.kq_fp8_act_unpack, "kq_fp8_act_unpack", stream, (act, codes, scales, values), int(K), _ptr(act),
-             int(M), _ptr(codes), _ptr(scales), _ptr(values), vdt)
+        vdt = names.flag.get(values.dtype, OUT_F32)
+        _flat(values, names.out[vdt][0], M * K, "values")
+    _fp8_call(lib.kq_fp8_act_unpack, "kq_fp8_act_unpack", stream, (act, codes, scales, values),
+              (K, act.data_ptr(), M, _ptr(codes), _ptr(scales), _ptr(values), vdt))
 
 
 def _fp8_y(Y, M: int, N: int, out_dtype: int) -> int:
-    import torch
-    return _rows(Y, (torch.bfloat16 if out_dtype == OUT_BF16 else torch.float32,), M, N, "Y")
+    dtypes = _names().out.get(out_dtype)
+    if dtypes is None:
+        raise ValueError(f"out_dtype must be OUT_F32 or OUT_BF16, got {out_dtype}")
+    return _rows(Y, dtypes, M, N, "Y")
 
 
 def fp8_gemm(layer: Fp8Layer, weights, act, M: int, Y, out_dtype: int = OUT_F32, stream=None) -> None:
@@ -613,8 +628,8 @@ def fp8_gemm(layer: Fp8Layer, weights, act, M: int, Y, out_dtype: int = OUT_F32,
     _fp8_weights(layer, weights)
     _fp8_act(act, layer.K, M)
     ldy = _fp8_y(Y, M, layer.N, out_dtype)
-    _fp8_run(lib.kq_fp8_gemm, "kq_fp8_gemm", stream, (weights, act, Y), layer.desc, _ptr(weights), _ptr(act),
-             int(M), _ptr(Y), ldy, int(out_dtype))
+    _fp8_call(lib.kq_fp8_gemm, "kq_fp8_gemm", stream, (weights, act, Y),
+              (layer._ref, weights.data_ptr(), act.data_ptr(), M, Y.data_ptr(), ldy, out_dtype))
 
 
 def fp8_gated_act(layer: Fp8Layer, weights, act, M: int, out_act, stream=None) -> None:
@@ -622,41 +637,40 @@ def fp8_gated_act(layer: Fp8Layer, weights, act, M: int, out_act, stream=None) -
     _fp8_weights(layer, weights)
     _fp8_act(act, layer.K, M)
     _fp8_act(out_act, layer.N, M, "out_act")
-    _fp8_run(lib.kq_fp8_gated_act, "kq_fp8_gated_act", stream, (weights, act, out_act), layer.desc, _ptr(weights),
-             _ptr(act), int(M), _ptr(out_act), out_act.numel())
+    _fp8_call(lib.kq_fp8_gated_act, "kq_fp8_gated_act", stream, (weights, act, out_act),
+              (layer._ref, weights.data_ptr(), act.data_ptr(), M, out_act.data_ptr(), out_act.numel()))
 
 
 def fp8_linear(layer: Fp8Layer, weights, X, Y, act, out_dtype: int = OUT_F32, stream=None) -> None:
-    """Quantize X (bf16 [M, K]) into act and run the layer into Y [M, N]."""
-    import torch
-    M = X.shape[0]
+    """The layer on X (bf16 [M, K]) into Y [M, N]; act is scratch."""
+    M, K = X.shape
     _fp8_weights(layer, weights)
-    ldx = _rows(X, (torch.bfloat16,), None, layer.K, "X")
+    ldx = _rows(X, _names().bf16, None, layer.K, "X")
     ldy = _fp8_y(Y, M, layer.N, out_dtype)
-    _fp8_act(act, layer.K, M)
-    _fp8_run(lib.kq_fp8_linear, "kq_fp8_linear", stream, (weights, X, Y, act), layer.desc, _ptr(weights), _ptr(X),
-             ldx, M, _ptr(Y), ldy, int(out_dtype), _ptr(act), act.numel())
+    _fp8_act(act, K, M)
+    _fp8_call(lib.kq_fp8_linear, "kq_fp8_linear", stream, (weights, X, Y, act),
+              (layer._ref, weights.data_ptr(), X.data_ptr(), ldx, M, Y.data_ptr(), ldy, out_dtype,
+               act.data_ptr(), act.numel()))
 
 
 def fp8_ffn(gated: Fp8Layer, gated_weights, down: Fp8Layer, down_weights, X, gamma, eps: float, Y, ws,
             out_dtype: int = OUT_F32, residual=None, stream=None) -> None:
     """A feed-forward block: rmsnorm of X + residual (gamma None: X as it is), the gated layer,
     the down projection into Y. ws: uint8, fp8_ffn_bytes(gated, down, M)."""
-    import torch
     M = X.shape[0]
     _fp8_weights(gated, gated_weights)
     _fp8_weights(down, down_weights)
     if not gated.gated or down.gated or down.K != gated.N or M < 1:
         raise ValueError("fp8_ffn takes a gated layer and a plain one with K equal to its N, and M >= 1")
-    _flat(ws, torch.uint8, fp8_act_bytes(gated.K, M) + fp8_act_bytes(gated.N, M), "ws")
-    ldx = _rows(X, (torch.bfloat16,), None, gated.K, "X")
+    _flat(ws, _names().u8, fp8_act_bytes(gated.K, M) + fp8_act_bytes(gated.N, M), "ws")
+    ldx = _rows(X, _names().bf16, None, gated.K, "X")
     if gamma is None and residual is not None:
         raise ValueError("residual needs gamma")
-    ldr, rdt = _fp8_norm(gamma, residual, M, gated.K) if gamma is not None else (0, OUT_F32)
+    res, ldr, rdt = _fp8_norm(gamma, residual, M, gated.K) if gamma is not None else (None, 0, OUT_F32)
     ldy = _fp8_y(Y, M, down.N, out_dtype)
-    _fp8_run(lib.kq_fp8_ffn, "kq_fp8_ffn", stream, (gated_weights, down_weights, X, gamma, residual, Y, ws),
-             gated.desc, _ptr(gated_weights), down.desc, _ptr(down_weights), _ptr(X), ldx, _ptr(residual), ldr,
-             rdt, _ptr(gamma), float(eps), M, _ptr(Y), ldy, int(out_dtype), _ptr(ws), ws.numel())
+    _fp8_call(lib.kq_fp8_ffn, "kq_fp8_ffn", stream, (gated_weights, down_weights, X, gamma, residual, Y, ws),
+              (gated._ref, gated_weights.data_ptr(), down._ref, down_weights.data_ptr(), X.data_ptr(), ldx, res, ldr,
+               rdt, _ptr(gamma), eps, M, Y.data_ptr(), ldy, out_dtype, ws.data_ptr(), ws.numel()))
 
 
 def fp8_last_device_error(act, stream=None) -> int:
