@@ -322,7 +322,8 @@ def make_ffn(kq, K, N, seed=0):
 
 
 @pytest.mark.parametrize("res", [None, "bf16", "f32"])
-@pytest.mark.parametrize("M,K,N", [(1, 256, 512), (9, 1152, 608), (100, 160, 288), (260, 512, 1056)])
+@pytest.mark.parametrize("M,K,N", [(1, 256, 512), (9, 1152, 608), (100, 160, 288), (260, 512, 1056), (2, 2080, 288),
+                                   (4, 1120, 160), (1, 12288, 64), (12, 1024, 160), (3, 32, 32)])
 def test_ffn_is_its_parts(cuda_device, M, K, N, res):
     """The block gives what its three calls give, bit for bit, and is near the float64 chain."""
     import torch
@@ -513,8 +514,14 @@ def test_output_on_the_input(cuda_device, M):
     gamma = torch.rand(K, device="cuda")
     ws = buf(kq.fp8_ffn_bytes(G, D, M))
     kq.fp8_ffn(G, gw, D, dw, X, gamma, EPS, want, ws, kq.OUT_BF16)
-    kq.fp8_ffn(G, gw, D, dw, X, gamma, EPS, X, ws, kq.OUT_BF16)
-    assert torch.equal(X, want)
+    inplace = X.clone()
+    kq.fp8_ffn(G, gw, D, dw, inplace, gamma, EPS, inplace, ws, kq.OUT_BF16)
+    assert torch.equal(inplace, want)
+    R = torch.randn(M, K, device="cuda").to(torch.bfloat16)
+    R1, R2 = R.clone(), R.clone()
+    kq.fp8_ffn(G, gw, D, dw, X, gamma, EPS, want, ws, kq.OUT_BF16, residual=R1)
+    kq.fp8_ffn(G, gw, D, dw, X, gamma, EPS, X, ws, kq.OUT_BF16, residual=R2)
+    assert torch.equal(X, want) and torch.equal(R1, R2) and not torch.equal(R1, R)
 
 
 @pytest.mark.parametrize("M", [2, 50, 130])
