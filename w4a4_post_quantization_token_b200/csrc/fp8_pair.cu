@@ -36,7 +36,6 @@ namespace fp8 {
 
 namespace {
 
-
 template <int BN>
 struct Pair {
   static constexpr bool kShared = BN == 256;
