@@ -598,3 +598,37 @@ def test_gate_far_from_zero(cuda_device, M, kind):
     z, u = A @ Wd.T, A @ Wud.T
     assert np.all(np.abs(z) > 7e4)
     np.testing.assert_allclose(_np(Y), np.where(z > 0, z, 0) * u, rtol=2.0 ** -18, atol=1e-30)
+
+
+@pytest.mark.parametrize("M", [8, 200])
+def test_silu_in_fp32(cuda_device, M):
+    """fp32 outputs of a gated layer whose two products are exact hold the activation to a few fp32
+    roundings, down to gates where it leaves the normal range.
+
+    exp(-|z|) is within 2 ulps (2^-22), the sum 1 + exp within 2^-24 and half of the exponential's
+    error (2^-23), the product z exp (for z < 0) within 2^-22 and a rounding of 2^-24, the quotient
+    within 2 ulps (2^-22), the product with u within 2^-24: (4 + 1 + 2 + 1 + 4 + 1) 2^-24 together.
+    Where the exponential is subnormal its 2 ulps are 2^-148, times z; the product there is half of
+    2^-149 off, the quotient 2 of them, both times u, and the result another half."""
+    import torch
+    import w4a4_post_quantization_token_b200 as kq
+    K, N = 32, 128
+    n = torch.arange(N)
+    X, W, Wu = torch.zeros(M, K), torch.zeros(K, N), torch.zeros(K, N)
+    X[:, 0], X[:, 1] = (torch.arange(M) % 8 + 1).float(), 1.0
+    sign = 1.0 - 2.0 * (n % 2)
+    W[0] = sign * (8 + n // 2 % 8) * torch.exp2((n // 16 % 4).float()) / 8      # 1 .. 15
+    W[1] = sign * (n % 5) / 8
+    Wu[1] = 3.0
+    X, W, Wu = (t.to(torch.bfloat16) for t in (X, W, Wu))
+    L = kq.Fp8Layer(K, N, gated=True)
+    w, (Wd, Wud) = packed(kq, L, W, Wu)
+    Y = torch.empty(M, N, device="cuda")
+    kq.fp8_linear(L, w, X.cuda(), Y, buf(kq.fp8_act_bytes(K, M)))
+    A = fp8.decode_rows(*fp8.encode_rows(_np(X)))
+    z, u = A @ Wd.T, A @ Wud.T
+    np.testing.assert_array_equal(z, _np(X) @ _np(W))       # nothing was rounded on the way
+    assert z.min() < -100 and z.max() > 100 and np.all(u == 3)
+    ref = fp8.activation(z, "silu") * u
+    bound = 13 * 2.0 ** -24 * np.abs(ref) + 2.0 ** -149 * ((2 * np.abs(z) + 2.5) * u + 1)
+    assert np.all(np.abs(_np(Y) - ref) <= bound)

@@ -110,11 +110,30 @@ __device__ __forceinline__ uint32_t block_byte(const float (&v)[8]) {
   return scale_byte(a);
 }
 
-// SiLU g / (1 + e^-g); GELU in its erf form, g erfc(-g / sqrt 2) / 2
-template <int ACT>
+// SiLU g / (1 + e^-g), from e^-|g|, which cannot overflow; GELU in its erf form,
+// g erfc(-g / sqrt 2) / 2. F32: for fp32 outputs the exponential is the full-precision one. The
+// approximate one rounds g log2 e first, so it is 2^-18 off at a gate of -60, which is nothing beside
+// the rounding to bf16 or E4M3; everywhere it cost 4096 x 256 -> 4096 in bf16 a sixth (32 -> 38 us).
+// The quotient, with a divisor of 1 to 2, is within 2 ulps and has no branch (the exact one has,
+// which keeps a thread's values from overlapping: 300 x 1152 -> 4608 in fp32 11 -> 24 us).
+template <int ACT, bool F32>
 __device__ __forceinline__ float gate_act(float g) {
-  if (ACT == 0) return __fdividef(g, 1.f + __expf(-g));
+  if (ACT == 0) {
+    const float e = F32 ? expf(-fabsf(g)) : __expf(-fabsf(g));
+    return __fdividef(g < 0.f ? g * e : g, 1.f + e);
+  }
   return 0.5f * g * erfcf(-0.70710678118654752f * g);
+}
+// v[i] = act(g[i]) u[i] of N outputs of type `out` (MmParams).
+template <int ACT, int N>
+__device__ __forceinline__ void gate(int out, const float* g, const float* u, float* v) {
+  if (ACT == 0 && out == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = gate_act<ACT, true>(g[i]) * u[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = gate_act<ACT, false>(g[i]) * u[i];
+  }
 }
 
 // --------------------------------------------------------------------- parameter blocks --

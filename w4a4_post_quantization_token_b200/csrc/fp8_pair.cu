@@ -371,11 +371,14 @@ __global__ void __launch_bounds__(Pair<BN>::kThreads, 1) k_mm_pair(const __grid_
           tmem_ld_32x32b_x32((buf == 0 ? g0 : u0) + 32 * c, r);
           tmem_ld_wait();
           if (owner && c == 1) release(buf);
+          float g[32], u[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const float o = __uint_as_float(r[i]), f = v[32 * c + i];
-            v[32 * c + i] = gate_act<ACT>(buf == 0 ? o : f) * (buf == 0 ? f : o);
+            g[i] = buf == 0 ? o : f;
+            u[i] = buf == 0 ? f : o;
           }
+          gate<ACT, 32>(p.out, g, u, v + 32 * c);
         }
         put_gated(p, v, stg, top, nt, half, q, m0, ok, lane);
       }

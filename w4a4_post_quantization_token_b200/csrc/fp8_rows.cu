@@ -369,9 +369,7 @@ __global__ void __launch_bounds__(Rows<BT, ACT >= 0, FUSED>::kThreads) k_rows_mm
               const float4 w = part[((s * C::kProducts + j) * cap + four + f - qs) * 128 + 32 * q + lane];
               v[j][4 * f] += w.x; v[j][4 * f + 1] += w.y; v[j][4 * f + 2] += w.z; v[j][4 * f + 3] += w.w;
             }
-        if (GATED)
-#pragma unroll
-          for (int i = 0; i < 4 * F; ++i) v[0][i] = gate_act<ACT>(v[0][i]) * v[C::kProducts - 1][i];
+        if (GATED) gate<ACT, 4 * F>(p.out, v[0], v[C::kProducts - 1], v[0]);
         store<4 * F, GATED>(p, v[0], 4 * four, ok ? min(min(4 * F, 4 * (qe - four)), tokens - 4 * four) : 0, n0, q, lane, top, tile);
       }
     }
@@ -381,14 +379,13 @@ __global__ void __launch_bounds__(Rows<BT, ACT >= 0, FUSED>::kThreads) k_rows_mm
 #pragma unroll
       for (int j = 0; j < C::kProducts; ++j) tmem_ld_32x32b_x16(tb + 64 * j + c, r[j]);
       tmem_ld_wait();
-      float v[16];
+      float v[C::kProducts][16];
 #pragma unroll
-      for (int t = 0; t < 16; ++t) {
-        v[t] = __uint_as_float(r[0][t]);
-        if (GATED)
-          v[t] = gate_act<ACT>(v[t]) * __uint_as_float(r[C::kProducts - 1][t]);
-      }
-      store<16, GATED>(p, v, c, ok ? min(16, tokens - c) : 0, n0, q, lane, top, tile);
+      for (int j = 0; j < C::kProducts; ++j)
+#pragma unroll
+        for (int t = 0; t < 16; ++t) v[j][t] = __uint_as_float(r[j][t]);
+      if (GATED) gate<ACT, 16>(p.out, v[0], v[C::kProducts - 1], v[0]);
+      store<16, GATED>(p, v[0], c, ok ? min(16, tokens - c) : 0, n0, q, lane, top, tile);
     }
   }
   tc_fence_before();
