@@ -443,8 +443,20 @@ kq_status kq_fp8_ffn(const kq_fp8_desc *gated, const void *gated_weights, const 
                      kq_stream_t stream);
 
 /* Synchronises `stream`, reports (KQ_ERR_DEVICE_TIMEOUT or KQ_OK) and clears the error word
- * of an 8-bit workspace. A call that fills the workspace clears it too. */
+ * of an 8-bit workspace. A call that fills the workspace clears it too. After a timeout, outputs whose
+ * sums were not complete have been left as they were; calls that read them give what that gives. */
 kq_status kq_fp8_last_device_error(void *act, kq_stream_t stream);
+
+/* Exercises the bounded waits of the 8-bit products without a fault: the product of kq_fp8_gemm (X_bf16
+ * null), of kq_fp8_linear, or of kq_fp8_gated_act (X_bf16 and Y null) in which no CTA loads the weights of
+ * the k_tile-th k-tile (128 features, from 0, counted over the CTA's tiles) that it takes, and every
+ * wait lasts limit_us microseconds (1 .. 1,000,000) at most. The outputs that need those weights stay
+ * as they are, kq_fp8_last_device_error on `act` reports KQ_ERR_DEVICE_TIMEOUT, and the context stays
+ * usable. A k_tile that no CTA reaches gives the ordinary product. Async on `stream`. */
+kq_status kq_fp8_debug_wait_timeout(const kq_fp8_desc *desc, const void *weights, const void *X_bf16,
+                                    int64_t ldx, int32_t M, void *Y, int64_t ldy, int32_t out_dtype, void *act,
+                                    size_t act_bytes, void *out_act, size_t out_act_bytes, int64_t k_tile,
+                                    uint32_t limit_us, kq_stream_t stream);
 
 /* Static string for a status code. */
 const char *kq_status_string(kq_status s);

@@ -126,3 +126,17 @@ def test_binding_checks():
         kq.fp8_prepare_weights(L(64, 64, True), X, act)
     with pytest.raises(ValueError, match="unsupported"):
         kq.fp8_gemm(L(40, 64), act, act, 4, X)
+
+
+def test_debug_wait_timeout():
+    d, plain = L(64, 64, True), L()
+
+    def t(d=plain, w=OK, X=None, ldx=0, M=4, Y=OK, ldy=64, dt=0, a=OK2, n=BIG, o=None, on=0, k=0, us=1000):
+        return lib.kq_fp8_debug_wait_timeout(d.desc, w, X, ldx, M, Y, ldy, dt, a, n, o, on, k, us, None)
+
+    assert t(k=-1) == 1 and t(us=0) == 1 and t(us=1000001) == 1 and t(w=None) == 1 and t(a=None) == 1 and t(M=0) == 1
+    assert t(Y=None) == 1 and t(dt=2) == 1 and t(ldy=66) == 3 and t(X=ODD, ldx=64) == 3 and t(X=OK, ldx=32) == 1
+    assert t(n=64) == 5 and t(d=L(40, 64)) == 2
+    assert t(o=OK, on=BIG, Y=None) == 1                                 # not gated
+    assert t(d=d, o=OK, on=BIG) == 1 and t(d=d, o=OK2, on=BIG, Y=None) == 1 and t(d=d, o=OK, on=64, Y=None) == 5
+    assert t(d=d, o=OK, on=BIG, X=OK, ldx=64, Y=None) == 1

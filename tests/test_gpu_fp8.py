@@ -632,3 +632,76 @@ def test_silu_in_fp32(cuda_device, M):
     ref = fp8.activation(z, "silu") * u
     bound = 13 * 2.0 ** -24 * np.abs(ref) + 2.0 ** -149 * ((2 * np.abs(z) + 2.5) * u + 1)
     assert np.all(np.abs(_np(Y) - ref) <= bound)
+
+
+def run_short_of_a_k_tile(kq, M, K, N, how, k_tile):
+    """The product with a k-tile's weights never loaded, then the ordinary one, on outputs filled with 0xAA
+    bytes: (bytes after the first, bytes after the second, 0xAA everywhere), status, seconds."""
+    import time
+
+    import torch
+    gated = how == "8bit"
+    L = kq.Fp8Layer(K, N, gated=gated)
+    w = buf(kq.fp8_weights_bytes(L))
+    kq.fp8_prepare_weights(L, weight(K, N, 1).cuda(), w, weight(K, N, 2).cuda() if gated else None)
+    X, act = tokens(M, K, 3).cuda(), buf(kq.fp8_act_bytes(K, M))
+    kq.fp8_quantize_act(X, act)
+    out = torch.full((kq.fp8_act_bytes(N, M) if gated else 2 * M * N,), 0xAA, dtype=torch.uint8, device="cuda")
+    Y = None if gated else out.view(torch.bfloat16).view(M, N)
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    kq.fp8_debug_wait_timeout(L, w, act, M, k_tile, 5000, X=X if how == "fused" else None, Y=Y,
+                              out_act=out if gated else None, out_dtype=kq.OUT_BF16)
+    status = kq.fp8_last_device_error(act)
+    seconds = time.perf_counter() - t0
+
+    def parts():
+        if gated:
+            return [torch.from_numpy(a) for a in unpack(kq, out, M, N)]
+        return [Y.view(torch.int16).cpu()]
+
+    short = parts()
+    if gated:
+        kq.fp8_gated_act(L, w, act, M, out)
+    elif how == "fused":
+        kq.fp8_linear(L, w, X, Y, act, kq.OUT_BF16)
+    else:
+        kq.fp8_gemm(L, w, act, M, Y, kq.OUT_BF16)
+    assert kq.fp8_last_device_error(act) == 0
+    return short, parts(), status, seconds
+
+
+@pytest.mark.parametrize("how,M,K,N", [
+    ("gemm", 5, 640, 9488), ("gemm", 5, 8192, 640), ("gemm", 20, 12288, 144), ("gemm", 64, 2560, 9488), ("gemm", 64, 4096, 400),
+    ("fused", 1, 4096, 256), ("fused", 20, 512, 272), ("fused", 2, 1152, 9488),
+    ("8bit", 2, 4096, 128), ("8bit", 20, 8192, 288), ("8bit", 64, 4096, 544), ("8bit", 9, 1536, 9600), ("8bit", 40, 1536, 9600),
+    ("gemm", 300, 1280, 528), ("gemm", 65, 4096, 400), ("gemm", 256, 12288, 528), ("gemm", 520, 1152, 656),
+    ("8bit", 130, 2080, 288), ("8bit", 1100, 160, 2080)])
+def test_a_wait_that_runs_out_leaves_the_outputs(cuda_device, how, M, K, N):
+    """Whichever k-tile does not come, the call ends in time, reports it, and stores none of the sums
+    that lack it; the context and the workspaces stay usable."""
+    import w4a4_post_quantization_token_b200 as kq
+    for k in (0, 1):
+        short, whole, status, seconds = run_short_of_a_k_tile(kq, M, K, N, how, k)
+        assert status == kq.ERR_DEVICE_TIMEOUT and 0.005 <= seconds < 2
+        for s, w in zip(short, whole):
+            assert bool((s == (0xAA if how == "8bit" else -21846)).all()) and not bool((w == s).all())
+
+
+@pytest.mark.parametrize("how,M,K,N,k", [("gemm", 2100, 160, 9296, 2), ("gemm", 2100, 160, 9296, 5), ("gemm", 1300, 640, 8208, 7),
+                                         ("8bit", 1100, 160, 4064, 3), ("8bit", 2300, 544, 4064, 11)])
+def test_tiles_before_a_wait_that_runs_out(cuda_device, how, M, K, N, k):
+    """Several tiles for each CTA pair: those whose sums came before are stored, right, and no others."""
+    import w4a4_post_quantization_token_b200 as kq
+    short, whole, status, seconds = run_short_of_a_k_tile(kq, M, K, N, how, k)
+    assert status == kq.ERR_DEVICE_TIMEOUT and 0.005 <= seconds < 2
+    for s, w in zip(short, whole):
+        left = s == (0xAA if how == "8bit" else -21846)
+        assert bool((left | (s == w)).all()) and 0.05 < left.double().mean() < 0.95
+
+
+def test_a_k_tile_past_the_last_is_not_missed(cuda_device):
+    import w4a4_post_quantization_token_b200 as kq
+    for how, M in (("gemm", 5), ("8bit", 130), ("fused", 3), ("gemm", 200)):
+        short, whole, status, _ = run_short_of_a_k_tile(kq, M, 640, 288, how, 1 << 40)
+        assert status == 0 and all(bool((s == w).all()) for s, w in zip(short, whole))

@@ -25,7 +25,7 @@ __all__ = ["KQError", "Layer", "lib", "library_path", "weights_bytes", "act_byte
            "Fp8Layer", "fp8_weights_bytes", "fp8_act_bytes", "fp8_ffn_bytes",
            "fp8_prepare_weights", "fp8_weights_pack", "fp8_weights_unpack", "fp8_quantize_act",
            "fp8_rmsnorm_act", "fp8_act_pack", "fp8_act_unpack", "fp8_gemm", "fp8_gated_act",
-           "fp8_linear", "fp8_ffn", "fp8_last_device_error", "ACT_SILU", "ACT_GELU"]
+           "fp8_linear", "fp8_ffn", "fp8_last_device_error", "fp8_debug_wait_timeout", "ACT_SILU", "ACT_GELU"]
 
 OUT_F32, OUT_BF16 = 0, 1
 ERR_DEVICE_TIMEOUT, ERR_LOWRANK_RANGE = 7, 9
@@ -50,7 +50,7 @@ SYMBOLS = ["kq_weights_bytes", "kq_act_bytes", "kq_prepare_ws_bytes", "kq_prepar
            "kq_fp8_prepare_weights", "kq_fp8_weights_pack", "kq_fp8_weights_unpack",
            "kq_fp8_quantize_act", "kq_fp8_rmsnorm_act", "kq_fp8_act_pack", "kq_fp8_act_unpack",
            "kq_fp8_gemm", "kq_fp8_gated_act", "kq_fp8_linear", "kq_fp8_ffn",
-           "kq_fp8_last_device_error"]
+           "kq_fp8_last_device_error", "kq_fp8_debug_wait_timeout"]
 
 
 class KQError(RuntimeError):
@@ -136,6 +136,8 @@ _sigs = {
     "kq_fp8_ffn": (ctypes.c_int, [_F, _P, _F, _P, _P, _I64, _P, _I64, _I32, _P, ctypes.c_float, _I32,
                                   _P, _I64, _I32, _P, _SZ, _P]),
     "kq_fp8_last_device_error": (ctypes.c_int, [_P, _P]),
+    "kq_fp8_debug_wait_timeout": (ctypes.c_int, [_F, _P, _P, _I64, _I32, _P, _I64, _I32, _P, _SZ, _P, _SZ, _I64,
+                                                 ctypes.c_uint32, _P]),
 }
 for _name, (_res, _args) in _sigs.items():
     _f = getattr(lib, _name)
@@ -680,3 +682,18 @@ def fp8_last_device_error(act, stream=None) -> int:
     _need(act, torch.uint8, 256, "act")
     with torch.cuda.device(act.device):
         return int(lib.kq_fp8_last_device_error(_ptr(act), _stream(stream)))
+
+
+def fp8_debug_wait_timeout(layer: Fp8Layer, weights, act, M: int, k_tile: int, limit_us: int, X=None, Y=None,
+                           out_act=None, out_dtype: int = OUT_F32, stream=None) -> None:
+    """The product of fp8_gemm, of fp8_linear (with X) or of fp8_gated_act (with out_act instead of Y) in
+    which every CTA leaves out the load of the weights of its k_tile-th k-tile and waits limit_us at most."""
+    _fp8_weights(layer, weights)
+    _fp8_act(act, layer.K, M)
+    ldx = 0 if X is None else _rows(X, _names().bf16, M, layer.K, "X")
+    ldy = 0 if out_act is not None else _fp8_y(Y, M, layer.N, out_dtype)
+    if out_act is not None:
+        _fp8_act(out_act, layer.N, M, "out_act")
+    _fp8_call(lib.kq_fp8_debug_wait_timeout, "kq_fp8_debug_wait_timeout", stream, (weights, X, Y, act, out_act),
+              (layer._ref, _ptr(weights), _ptr(X), ldx, int(M), _ptr(Y), ldy, out_dtype, _ptr(act), act.numel(),
+               _ptr(out_act), 0 if out_act is None else out_act.numel(), int(k_tile), int(limit_us)))

@@ -175,6 +175,8 @@ struct MmParams {
   int dependent;              // launched as a programmatic dependent of the kernel that writes
                               //   the activations, whose predecessors had ended
   uint32_t* err;
+  uint64_t wait_ns;           // limit of each wait on a barrier
+  int withhold;               // >= 0: this k-tile of a CTA's weights is not loaded (a wait runs out)
 };
 
 cudaError_t launch_rows(const NormParams& p, bool norm, int res_kind, cudaStream_t st);

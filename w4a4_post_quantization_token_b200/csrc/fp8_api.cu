@@ -84,10 +84,13 @@ kq_status run_rows(int32_t K, const void* X, int64_t ldx, const Norm* n, int32_t
   return fp8::launch_rows(p, n != nullptr, res, st) == cudaSuccess ? KQ_OK : KQ_ERR_CUDA;
 }
 
+// A run whose waits are to end early (kq_fp8_debug_wait_timeout).
+struct Withhold { int k_tile = -1; uint64_t wait_ns = kWaitLimitNs; };
+
 // Y (out 0 / 1) or the 8-bit workspace `oact` (out 2) from the activations in `act`.
 kq_status run_mm(const kq_fp8_desc* d, const void* weights, uint8_t* act, int32_t M, int out, void* Y,
                  int64_t ldy, uint8_t* oact, uint32_t* err, bool dependent, const DeviceInfo& di, cudaStream_t st,
-                 const void* xb = nullptr, int64_t ldx = 0) {
+                 const void* xb = nullptr, int64_t ldx = 0, const Withhold& wh = Withhold()) {
   const fp8::WLayout W = wlayout(d);
   const fp8::ALayout A = fp8::ALayout::make(M, d->K);
   const uint8_t* w = static_cast<const uint8_t*>(weights);
@@ -112,6 +115,8 @@ kq_status run_mm(const kq_fp8_desc* d, const void* weights, uint8_t* act, int32_
   p.y = Y;
   p.ldy = ldy;
   p.err = err;
+  p.wait_ns = wh.wait_ns;
+  p.withhold = wh.k_tile;
   if (out == 2) {
     const fp8::ALayout O = fp8::ALayout::make(M, d->N);
     p.ocodes = oact + O.codes;
@@ -358,6 +363,32 @@ kq_status kq_fp8_ffn(const kq_fp8_desc* gated, const void* gated_weights, const 
   if ((s = run_rows(gated->K, X_bf16, ldx, gamma ? &n : nullptr, M, a, st)) != KQ_OK) return s;
   if ((s = run_mm(gated, gated_weights, a, M, 2, nullptr, 0, h, err_word(a), true, di, st)) != KQ_OK) return s;
   return run_mm(down, down_weights, h, M, out_dtype == KQ_OUT_BF16 ? 1 : 0, Y, ldy, nullptr, err_word(a), true, di, st);
+}
+
+kq_status kq_fp8_debug_wait_timeout(const kq_fp8_desc* desc, const void* weights, const void* X_bf16, int64_t ldx,
+                                    int32_t M, void* Y, int64_t ldy, int32_t out_dtype, void* act, size_t act_bytes,
+                                    void* out_act, size_t out_act_bytes, int64_t k_tile, uint32_t limit_us,
+                                    kq_stream_t stream) {
+  kq_status s = check_fp8(desc);
+  if (s != KQ_OK) return s;
+  if (!weights || k_tile < 0 || limit_us == 0 || limit_us > 1000000u) return KQ_ERR_INVALID_ARG;
+  if (!aligned(weights)) return KQ_ERR_ALIGNMENT;
+  if ((s = check_act(act, act_bytes, desc->K, M)) != KQ_OK) return s;
+  if (X_bf16 && (s = check_rows(X_bf16, ldx, desc->K, 2)) != KQ_OK) return s;
+  if (out_act) {
+    if (!desc->gated || act == out_act || X_bf16 || Y) return KQ_ERR_INVALID_ARG;
+    if ((s = check_width(desc->N)) != KQ_OK || (s = check_act(out_act, out_act_bytes, desc->N, M)) != KQ_OK) return s;
+  } else if ((s = check_y(Y, ldy, desc->N, out_dtype)) != KQ_OK) {
+    return s;
+  }
+  DeviceInfo di;
+  if ((s = current_device(&di)) != KQ_OK) return s;
+  Withhold wh;
+  wh.k_tile = k_tile > INT32_MAX ? -1 : static_cast<int>(k_tile);
+  wh.wait_ns = uint64_t{1000} * limit_us;
+  return run_mm(desc, weights, static_cast<uint8_t*>(act), M, out_act ? 2 : out_dtype == KQ_OUT_BF16 ? 1 : 0, Y, ldy,
+                static_cast<uint8_t*>(out_act), err_word(act), false, di, reinterpret_cast<cudaStream_t>(stream), X_bf16,
+                ldx, wh);
 }
 
 kq_status kq_fp8_last_device_error(void* act, kq_stream_t stream) {

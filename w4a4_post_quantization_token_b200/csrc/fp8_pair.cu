@@ -17,6 +17,10 @@
 // and 192 .. 447): the epilogue reads the shared 64 columns first, and the next tile's MMAs start
 // when those are out, some 1800 cycles after the last MMA.
 //
+// A wait that runs out ends the kernel as in k_rows_mm: the MMA issuer waits for its MMAs and for the
+// loads of both CTAs that are under way, an epilogue warp stores nothing from the tile whose
+// accumulators did not come, frees none and leaves.
+//
 // Where tiles are fewer than pairs of SMs, two or four pairs share K and exchange partial sums as in
 // k_rows_mm (SPLIT).
 //
@@ -130,30 +134,34 @@ __device__ __forceinline__ void put_values(const MmParams& p, const float (&v)[C
   }
 }
 
-// Outputs 64 half .. 64 half + 63 of gated tile nt, one token per thread (token m0 + lane).
-__device__ __forceinline__ void put_gated(const MmParams& p, const float (&v)[64], uint8_t* stg, uint32_t* top, int nt,
+// Outputs 64 half .. 64 half + 63 of gated tile nt, one token per thread (token m0 + lane). `ok`, the
+// same in all lanes: the sums are there; returns whether this is so in the warps that it met.
+__device__ __forceinline__ bool put_gated(const MmParams& p, const float (&v)[64], uint8_t* stg, uint32_t* top, int nt,
                                           int half, int q, int m0, bool ok, int lane) {
   const int n0 = nt * 128 + 64 * half;
   if (p.out != 2) {
     put_values(p, v, stg, n0, m0, ok, lane);
-    return;
+    return ok;
   }
   // a block is the 128 outputs of a token in this tile: its largest value from both halves
   uint32_t a = 0;
 #pragma unroll
   for (int i = 0; i < 64; ++i)
     if (n0 + i < p.N) a = max(a, abs_bits(v[i]));
+  if (!ok) a = ~0u;                                                  // no magnitude
   top[128 * half + 32 * q + lane] = a;
   asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");
   a = max(a, top[128 * (half ^ 1) + 32 * q + lane]);
   asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");
+  if (a == ~0u) return false;
   const uint32_t byte = scale_byte(a);
   const float is = inv_scale(byte);
   uint32_t w[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) w[i] = e4m3x4(v[4 * i] * is, v[4 * i + 1] * is, v[4 * i + 2] * is, v[4 * i + 3] * is);
-  put_rows(w, stg, p.ocodes + static_cast<int64_t>(m0) * p.N + n0, p.N, p.N - n0, ok ? min(32, p.M - m0) : 0, lane);
-  if (ok && half == 0 && m0 + lane < p.M) p.osf[sf_offset(m0 + lane, nt, p.okatoms)] = static_cast<uint8_t>(byte);
+  put_rows(w, stg, p.ocodes + static_cast<int64_t>(m0) * p.N + n0, p.N, p.N - n0, min(32, p.M - m0), lane);
+  if (half == 0 && m0 + lane < p.M) p.osf[sf_offset(m0 + lane, nt, p.okatoms)] = static_cast<uint8_t>(byte);
+  return true;
 }
 
 // ACT: -1 plain, 0 SiLU-gated, 1 GELU-gated. SPLIT: K is shared by the 2 or 4 pairs of a cluster.
@@ -169,7 +177,9 @@ __global__ void __launch_bounds__(Pair<BN>::kThreads, 1) k_mm_pair(const __grid_
   uint64_t* empty = full + C::kStages;
   uint64_t* acc_full = empty + C::kStages;
   uint64_t* acc_free = acc_full + 2;                                 // used in the first CTA
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_free + 2);
+  uint64_t* mma_done = acc_free + 2;                                 // in the first CTA, after a wait ran out
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  volatile uint32_t* bad = tmem_slot + 1;                            // SPLIT: sums of this CTA's outputs are missing
   uint8_t* ring = smem + C::kRingOff;
   uint8_t* sfring = smem + C::kSfOff;
   uint32_t* top = reinterpret_cast<uint32_t*>(smem + C::kTopOff);
@@ -186,6 +196,8 @@ __global__ void __launch_bounds__(Pair<BN>::kThreads, 1) k_mm_pair(const __grid_
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
     for (int b = 0; b < 2; ++b) { mbar_init(&acc_full[b], 1); mbar_init(&acc_free[b], 16); }
+    mbar_init(mma_done, 1);
+    *bad = 0;
     fence_mbar_init();
     prefetch_tmap(&p.tmap_w[0]);
     if (GATED) prefetch_tmap(&p.tmap_w[1]);
@@ -211,6 +223,7 @@ __global__ void __launch_bounds__(Pair<BN>::kThreads, 1) k_mm_pair(const __grid_
     const uint32_t sf0 = smem_u32(sfring) + (tokens ? 0 : 512);
     const uint32_t bar0 = mapa_shared(smem_u32(&full[0]), lead), mine0 = smem_u32(&full[0]);
     const uint32_t expect = tokens && rank == 0 ? one : 0u;
+    const int64_t skip = tokens ? -1 : p.withhold;
     uint32_t off = 0, st = ring0, sf = sf0;
     int s = 0;
     uint32_t ph = 1;
@@ -226,13 +239,14 @@ __global__ void __launch_bounds__(Pair<BN>::kThreads, 1) k_mm_pair(const __grid_
       const int xa = min(m0 / 128, xb) * ka, wa0 = (GATED ? nt : nt * BN / 128) * ka,
                 wa1 = (GATED ? nt : min(nt * BN / 128 + 1, nb)) * ka;
       for (int kt = kt0; kt < kt1; ++kt, ++it) {
-        if (it >= C::kStages && !mbar_wait(&empty[s], ph, p.err, KQ_DEV_ERR_TIMEOUT_EMPTY)) {
+        if (it == C::kStages) grid_dep_wait();
+        if (it >= C::kStages && !mbar_wait(&empty[s], ph, p.err, KQ_DEV_ERR_TIMEOUT_EMPTY, p.wait_ns)) {
           ok = false;
           break;
         }
         const bool atom = (kt & 3) == 0 || (SPLIT && kt == kt0);
         expect_tx_if(expect, mine0 + off, 2 * (C::kStageBytes + (atom ? C::kSfBytes : 0u)));
-        tma_load_pair_if(one, st, map, kt * kBlk, y, bar0 + off);
+        tma_load_pair_if(it == skip ? 0u : one, st, map, kt * kBlk, y, bar0 + off);
         if (atom) {
           if (tokens) {
             tma_load_pair_if(one, sf, &p.tmap_sfx, 0, xa + (kt >> 2), bar0 + off);
@@ -247,9 +261,6 @@ __global__ void __launch_bounds__(Pair<BN>::kThreads, 1) k_mm_pair(const __grid_
         if (++s == C::kStages) { s = 0; ph ^= 1u; off = 0; st = ring0; sf = sf0; }
       }
     }
-    // the first CTA's barriers count the loads of both; the peer leaves after the cluster barrier
-    // below, so after this wait
-    if (!ok && rank == 0 && one) drain_ring(full, C::kStages, it);
   } else if (warp == 1) {
     if (rank == 0) {
       const uint32_t one = elect_one();
@@ -259,12 +270,14 @@ __global__ void __launch_bounds__(Pair<BN>::kThreads, 1) k_mm_pair(const __grid_
       uint32_t bar = smem_u32(empty), f = tmem + C::kSfCol + C::kSfSet * (C::kSets - 1);
       int s = 0, local = 0, set = C::kSets - 1;
       uint32_t ph = 0;
-      bool ok = true;
-      for (int tile = first; tile < T && ok; tile += step, ++local) {
+      const int64_t per = kt1 - kt0;
+      int64_t stop = -1;                                             // k-tiles taken when a wait ran out
+      grid_dep_wait();
+      for (int tile = first; tile < T && stop < 0; tile += step, ++local) {
         const int buf = local & 1;
         const int since = C::kShared && buf ? local - 1 : local - 2;  // tiles since acc_free[buf]'s first phase
-        if (since >= 0 && !mbar_wait_cluster(&acc_free[buf], (since >> 1) & 1, p.err, KQ_DEV_ERR_TIMEOUT_ACC)) {
-          ok = false;
+        if (since >= 0 && !mbar_wait_cluster(&acc_free[buf], (since >> 1) & 1, p.err, KQ_DEV_ERR_TIMEOUT_ACC, p.wait_ns)) {
+          stop = local * per;
           break;
         }
         tc_fence_after();
@@ -277,8 +290,8 @@ __global__ void __launch_bounds__(Pair<BN>::kThreads, 1) k_mm_pair(const __grid_
         }
         uint32_t acc = 0;
         for (int kt = kt0; kt < kt1; ++kt) {
-          if (!mbar_wait(&full[s], ph, p.err, KQ_DEV_ERR_TIMEOUT_FULL)) {
-            ok = false;
+          if (!mbar_wait(&full[s], ph, p.err, KQ_DEV_ERR_TIMEOUT_FULL, p.wait_ns)) {
+            stop = local * per + kt - kt0;
             break;
           }
           tc_fence_after();
@@ -303,7 +316,13 @@ __global__ void __launch_bounds__(Pair<BN>::kThreads, 1) k_mm_pair(const __grid_
           bar += 8;
           if (++s == C::kStages) { s = 0; ph ^= 1u; so = 0; sd = sd0; bar = smem_u32(empty); }
         }
-        commit_if<true>(one, smem_u32(&acc_full[buf]), both);
+        if (stop < 0) commit_if<true>(one, smem_u32(&acc_full[buf]), both);
+      }
+      if (stop >= 0) {
+        // the barriers count the loads of both CTAs; the peer leaves after the cluster barrier below
+        commit_if<true>(one, smem_u32(mma_done), static_cast<uint16_t>(1u << lead));
+        drain_after(full, C::kStages, stop, cdiv(T - first, step) * per, p.wait_ns);
+        mbar_wait(mma_done, 0, nullptr, 0u, p.wait_ns);
       }
     }
   } else {
@@ -324,13 +343,14 @@ __global__ void __launch_bounds__(Pair<BN>::kThreads, 1) k_mm_pair(const __grid_
       const int m0 = mt * 256 + 128 * static_cast<int>(rank) + 32 * q;
       const int buf = local & 1;
       const bool owner = half != buf;
-      const bool ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (local >> 1) & 1, p.err, KQ_DEV_ERR_TIMEOUT_ACC));
+      bool ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (local >> 1) & 1, p.err, KQ_DEV_ERR_TIMEOUT_ACC, p.wait_ns));
+      if (!GATED && !ok) break;
       tc_fence_after();
       const uint32_t tb = tmem + static_cast<uint32_t>(buf) * C::kAccStride + (static_cast<uint32_t>(32 * q) << 16);
       auto release = [&](int b) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(free0 + 8u * static_cast<uint32_t>(b));
+        if (lane == 0 && ok) mbar_arrive_cluster(free0 + 8u * static_cast<uint32_t>(b));
       };
       if (!GATED) {
         // chunks of 64 (or 32) columns; the shared ones first: 192 .. 255 in the second half of
@@ -380,7 +400,8 @@ __global__ void __launch_bounds__(Pair<BN>::kThreads, 1) k_mm_pair(const __grid_
           }
           gate<ACT, 32>(p.out, g, u, v + 32 * c);
         }
-        put_gated(p, v, stg, top, nt, half, q, m0, ok, lane);
+        ok = put_gated(p, v, stg, top, nt, half, q, m0, ok, lane);
+        if (!ok) break;
       }
     }
   }
@@ -392,7 +413,7 @@ __global__ void __launch_bounds__(Pair<BN>::kThreads, 1) k_mm_pair(const __grid_
     const int q = warp & 3, nq = 4 / splits;
     bool ok = true;
     if (epi) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[0], 0, p.err, KQ_DEV_ERR_TIMEOUT_ACC));
+      ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[0], 0, p.err, KQ_DEV_ERR_TIMEOUT_ACC, p.wait_ns));
       tc_fence_after();
     }
     __syncwarp();
@@ -412,9 +433,11 @@ __global__ void __launch_bounds__(Pair<BN>::kThreads, 1) k_mm_pair(const __grid_
           st_shared_cluster_v4(at + 512u * static_cast<uint32_t>(c / 4 + j), r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
       }
     }
+    if (!ok && lane < 2 * splits) st_shared_cluster_u32(mapa_shared(smem_u32(const_cast<uint32_t*>(bad)), lane), 1u);
     __syncwarp();
     cluster_sync();
     if (epi) {
+      ok = *bad == 0;
       const float4* part = reinterpret_cast<const float4*>(ring) + lane;
       int mt, nt;
       pair_tile(first, MT, NT, mt, nt);

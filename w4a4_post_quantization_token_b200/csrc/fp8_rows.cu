@@ -17,6 +17,10 @@
 //             product, a commit that frees the stage.
 //   warps 2-5 epilogue: thread = output feature; a warp writes 32 neighbouring features of one
 //             token at a time.
+// A wait that runs out ends the kernel without an output: the MMA issuer does not commit the
+// accumulators, waits for its MMAs and for the loads under way, and the epilogue's own wait for the
+// accumulators runs out too. It stores nothing then, and neither does a CTA that lacks its sums.
+// The clocks of all waits start once the kernel before this one has ended.
 // FUSED: the activations are bf16 and the kernel encodes its share of K of them itself, while the
 // first weights arrive: warps 2-5 and 7-14 write codes (in the swizzled layout of a TMA load) and
 // scale bytes to shared memory. Every CTA of the same share does the same work over again, which
@@ -88,13 +92,14 @@ struct Rows {
 // One thread's feature n0 + 32 q + lane of T tokens from `token`, `lim` of which exist. The four
 // epilogue warps call it together. A block of the 8-bit output is the CTA's 128 features of one
 // token: its largest value is found across the warps (`top` [4][16]), the codes are put together
-// in `tile` [T][128] and written 16 to a store.
+// in `tile` [T][128] and written 16 to a store; nothing is written if `bad` was set in any of them.
 template <int T, bool GATED>
 __device__ __forceinline__ void store(const MmParams& p, const float* v, int token, int lim, int n0, int q, int lane,
-                                      uint32_t* top, uint8_t* tile) {
+                                      uint32_t* top, uint8_t* tile, const volatile uint32_t* bad) {
   const int n = n0 + 32 * q + lane;
   if (GATED && p.out == 2) {
     asm volatile("bar.sync 1, 128;" ::: "memory");          // the last call's maxima and codes were read
+    if (*bad) lim = 0;
     uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < T; ++j) {
@@ -181,7 +186,9 @@ __global__ void __launch_bounds__(Rows<BT, ACT >= 0, FUSED>::kThreads) k_rows_mm
   uint64_t* empty = full + C::kStages;
   uint64_t* acc_full = empty + C::kStages;
   uint64_t* x_ready = acc_full + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(x_ready + 1);
+  uint64_t* mma_done = x_ready + 1;                                      // after a wait ran out
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  volatile uint32_t* bad = tmem_slot + 1;                                // sums of this CTA's outputs are missing
   uint32_t* top = reinterpret_cast<uint32_t*>(smem + 512);               // [4 warps][16 tokens]
   uint8_t* ring = smem + 1024;
 
@@ -198,6 +205,8 @@ __global__ void __launch_bounds__(Rows<BT, ACT >= 0, FUSED>::kThreads) k_rows_mm
     for (int s = 0; s < C::kStages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
     mbar_init(acc_full, 1);
     mbar_init(x_ready, 32 * kEncWarps);
+    mbar_init(mma_done, 1);
+    *bad = 0;
     fence_mbar_init();
     prefetch_tmap(&p.tmap_w[0]);
     if (GATED) prefetch_tmap(&p.tmap_w[1]);
@@ -220,23 +229,25 @@ __global__ void __launch_bounds__(Rows<BT, ACT >= 0, FUSED>::kThreads) k_rows_mm
     const uint8_t* sfw[2] = {p.sfw[0] + static_cast<size_t>(blockIdx.x) * p.katoms * 512u,
                              GATED ? p.sfw[1] + static_cast<size_t>(blockIdx.x) * p.katoms * 512u : nullptr};
     uint32_t st = smem_u32(ring), bar = smem_u32(full);
-    int s = 0, i = 0;
+    const int skip = p.withhold;
+    int s = 0;
     uint32_t ph = 1;
-    for (; i < n_kt; ++i) {
-      if (i >= C::kStages && !mbar_wait(&empty[s], ph, p.err, KQ_DEV_ERR_TIMEOUT_EMPTY)) break;
+    for (int i = 0; i < n_kt; ++i) {
+      if (i == C::kStages) grid_dep_wait();
+      if (i >= C::kStages && !mbar_wait(&empty[s], ph, p.err, KQ_DEV_ERR_TIMEOUT_EMPTY, p.wait_ns)) break;
       const int kt = kt0 + i;
       const bool atom = (kt & 3) == 0 || i == 0;
+      const uint32_t load = i == skip ? 0u : one;
       expect_tx_if(one, bar, C::kSfOff + (atom ? C::kSfAtoms * 512u : 0u));
 #pragma unroll
       for (int j = 0; j < C::kProducts; ++j) {
-        tma_load_if(one, st + j * C::kABytes, &p.tmap_w[j], kt * kBlk, n0, bar);
+        tma_load_if(load, st + j * C::kABytes, &p.tmap_w[j], kt * kBlk, n0, bar);
         if (atom) bulk_load_if(one, st + C::kSfOff + j * 512, sfw[j] + static_cast<size_t>(kt >> 2) * 512u, 512, bar);
       }
       st += C::kStageBytes;
       bar += 8;
       if (++s == C::kStages) { s = 0; ph ^= 1u; st = smem_u32(ring); bar = smem_u32(full); }
     }
-    if (i < n_kt && one) drain_ring(full, C::kStages, i);
   } else if (warp == 6) {
     if (!FUSED) {
       grid_dep_wait();
@@ -247,7 +258,7 @@ __global__ void __launch_bounds__(Rows<BT, ACT >= 0, FUSED>::kThreads) k_rows_mm
       int s = 0;
       uint32_t ph = 1;
       for (int i = 0; i < n_kt; ++i) {
-        if (i >= C::kStages && !mbar_wait(&empty[s], ph, p.err, KQ_DEV_ERR_TIMEOUT_EMPTY)) break;
+        if (i >= C::kStages && !mbar_wait(&empty[s], ph, p.err, KQ_DEV_ERR_TIMEOUT_EMPTY, p.wait_ns)) break;
         const int kt = kt0 + i;
         tma_load_if(one, st, &p.tmap_x, kt * kBlk, 0, bar);
         if ((kt & 3) == 0 || i == 0)
@@ -266,11 +277,13 @@ __global__ void __launch_bounds__(Rows<BT, ACT >= 0, FUSED>::kThreads) k_rows_mm
     uint64_t so = 0;                                       // the stage's offset in descriptor units
     uint64_t bo = 0, xs = sdesc_plain_rows16(smem_u32(xsf));
     uint32_t bar = smem_u32(empty);
-    int s = 0, set = 2;
+    int s = 0, set = 2, i = 0;
     uint32_t ph = 0, acc = 0;
-    bool ok = !FUSED || mbar_wait(x_ready, 0, p.err, KQ_DEV_ERR_TIMEOUT_FULL);
-    for (int i = 0; i < n_kt && ok; ++i) {
-      if (!mbar_wait(&full[s], ph, p.err, KQ_DEV_ERR_TIMEOUT_FULL)) break;
+    grid_dep_wait();
+    bool ok = !FUSED || mbar_wait(x_ready, 0, p.err, KQ_DEV_ERR_TIMEOUT_FULL, p.wait_ns);
+    for (; i < n_kt && ok; ++i) {
+      ok = mbar_wait(&full[s], ph, p.err, KQ_DEV_ERR_TIMEOUT_FULL, p.wait_ns);
+      if (!ok) break;
       tc_fence_after();
       const int kt = kt0 + i;
       if ((kt & 3) == 0 || i == 0) {
@@ -299,7 +312,11 @@ __global__ void __launch_bounds__(Rows<BT, ACT >= 0, FUSED>::kThreads) k_rows_mm
       bar += 8;
       if (++s == C::kStages) { s = 0; ph ^= 1u; so = 0; bar = smem_u32(empty); }
     }
-    commit_if<false>(one, smem_u32(acc_full));
+    commit_if<false>(one, smem_u32(ok ? acc_full : mma_done));
+    if (!ok) {
+      drain_after(full, C::kStages, i, n_kt, p.wait_ns);
+      mbar_wait(mma_done, 0, nullptr, 0u, p.wait_ns);
+    }
   }
   const int q = warp & 3;                                  // TMEM lane quadrant
   const uint32_t tb = tmem + (static_cast<uint32_t>(32 * q) << 16);
@@ -317,7 +334,8 @@ __global__ void __launch_bounds__(Rows<BT, ACT >= 0, FUSED>::kThreads) k_rows_mm
   }
   if (epi) {
     if (p.out == 2 && blockIdx.x == 0 && rank == 0 && threadIdx.x == 64) *p.oerr = 0u;
-    ok = __all_sync(0xffffffffu, mbar_wait(acc_full, 0, p.err, KQ_DEV_ERR_TIMEOUT_ACC));
+    ok = __all_sync(0xffffffffu, mbar_wait(acc_full, 0, p.err, KQ_DEV_ERR_TIMEOUT_ACC, p.wait_ns));
+    if (!ok) *bad = 1u;
     tc_fence_after();
   }
   if (splits > 1) {
@@ -352,9 +370,11 @@ __global__ void __launch_bounds__(Rows<BT, ACT >= 0, FUSED>::kThreads) k_rows_mm
         }
       }
     }
+    if (!ok && lane < splits) st_shared_cluster_u32(mapa_shared(smem_u32(const_cast<uint32_t*>(bad)), lane), 1u);
     __syncwarp();
     cluster_sync();
     if (epi) {
+      ok = *bad == 0;
       const int qs = Q * rank / splits, qe = Q * (rank + 1) / splits;
       // up to four fours to a call of store, which the 8-bit output makes a meeting of the warps
       constexpr int F = BT <= 16 ? 1 : 4;
@@ -370,7 +390,7 @@ __global__ void __launch_bounds__(Rows<BT, ACT >= 0, FUSED>::kThreads) k_rows_mm
               v[j][4 * f] += w.x; v[j][4 * f + 1] += w.y; v[j][4 * f + 2] += w.z; v[j][4 * f + 3] += w.w;
             }
         if (GATED) gate<ACT, 4 * F>(p.out, v[0], v[C::kProducts - 1], v[0]);
-        store<4 * F, GATED>(p, v[0], 4 * four, ok ? min(min(4 * F, 4 * (qe - four)), tokens - 4 * four) : 0, n0, q, lane, top, tile);
+        store<4 * F, GATED>(p, v[0], 4 * four, ok ? min(min(4 * F, 4 * (qe - four)), tokens - 4 * four) : 0, n0, q, lane, top, tile, bad);
       }
     }
   } else if (epi) {
@@ -385,7 +405,7 @@ __global__ void __launch_bounds__(Rows<BT, ACT >= 0, FUSED>::kThreads) k_rows_mm
 #pragma unroll
         for (int t = 0; t < 16; ++t) v[j][t] = __uint_as_float(r[j][t]);
       if (GATED) gate<ACT, 16>(p.out, v[0], v[C::kProducts - 1], v[0]);
-      store<16, GATED>(p, v[0], c, ok ? min(16, tokens - c) : 0, n0, q, lane, top, tile);
+      store<16, GATED>(p, v[0], c, ok ? min(16, tokens - c) : 0, n0, q, lane, top, tile, bad);
     }
   }
   tc_fence_before();

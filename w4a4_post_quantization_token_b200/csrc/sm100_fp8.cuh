@@ -117,12 +117,15 @@ __device__ __forceinline__ void cluster_arrive() {
 __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void st_shared_cluster_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ void st_shared_cluster_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 // mbar_wait for a barrier on which other CTAs of the cluster arrive.
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, uint32_t* err,
-                                                  uint32_t code) {
+                                                  uint32_t code, uint64_t limit_ns) {
   const uint32_t a = smem_u32(bar);
   uint64_t t0 = 0;
   for (uint32_t i = 0;; ++i) {
@@ -134,11 +137,19 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
         : "=r"(ok) : "r"(a), "r"(parity) : "memory");
     if (ok) return true;
     if (i == 0) t0 = globaltimer_ns();
-    else if ((i & 255u) == 0u && globaltimer_ns() - t0 > kWaitLimitNs) {
+    else if ((i & 255u) == 0u && globaltimer_ns() - t0 > limit_ns) {
       if (err) atomicOr(err, code);
       return false;
     }
   }
+}
+
+// drain_ring for an MMA issuer whose wait ran out after `taken` of `total` k-tiles: waits, limit_ns at
+// most for each slot and without reporting, for the loads that are under way or about to be (a
+// producer is a ring ahead), since no copy may still land when the CTA goes on.
+__device__ __forceinline__ void drain_after(uint64_t* full, int stages, int64_t taken, int64_t total, uint64_t limit_ns) {
+  for (int64_t j = taken; j < min(taken + stages, total); ++j)
+    mbar_wait(&full[j % stages], static_cast<uint32_t>(j / stages) & 1u, nullptr, 0u, limit_ns);
 }
 
 // Each thread of the warp reads 16 consecutive 32-bit columns of its own TMEM lane.
