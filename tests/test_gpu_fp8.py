@@ -705,3 +705,36 @@ def test_a_k_tile_past_the_last_is_not_missed(cuda_device):
     for how, M in (("gemm", 5), ("8bit", 130), ("fused", 3), ("gemm", 200)):
         short, whole, status, _ = run_short_of_a_k_tile(kq, M, 640, 288, how, 1 << 40)
         assert status == 0 and all(bool((s == w).all()) for s, w in zip(short, whole))
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+@pytest.mark.parametrize("M,K,N", [(17, 32, 32), (20, 512, 288), (31, 8192, 672), (32, 2080, 9632), (33, 64, 96), (48, 160, 416),
+                                   (64, 4096, 544), (64, 1152, 9568), (12, 4096, 160), (16, 96, 9504)])
+def test_8bit_output_of_few_tokens(cuda_device, M, K, N, kind):
+    """Every token tile of the few-token kernel, K whole and split, last blocks of 32 to 96 outputs: codes
+    within half a step of E4M3 under the block's own scale, which is the smallest that holds the
+    block's largest value; nothing past the workspace is written."""
+    import torch
+    import w4a4_post_quantization_token_b200 as kq
+    X, W, Wu = tokens(M, K, K + 1), weight(K, N, 3), weight(K, N, 4)
+    L = kq.Fp8Layer(K, N, gated=True, activation=kind)
+    w, (Wd, Wud) = packed(kq, L, W, Wu)
+    act = buf(kq.fp8_act_bytes(K, M))
+    A = fp8.decode_rows(*fp8.encode_rows(_np(X)))
+    z, u = A @ Wd.T, A @ Wud.T
+    ref = fp8.activation(z, kind) * u
+    bound = gated_bound(z, u, accumulation(A, Wd), accumulation(A, Wud), kind)
+    h = torch.full((kq.fp8_act_bytes(N, M + 64),), 0xAA, dtype=torch.uint8, device="cuda")
+    kq.fp8_quantize_act(X.cuda(), act)
+    kq.fp8_gated_act(L, w, act, M, h)
+    assert kq.fp8_last_device_error(act) == 0
+    c, s = unpack(kq, h, M, N)
+    scale = np.repeat(np.ldexp(1.0, s.astype(int) - 127), 128, 1)[:, :N]
+    assert np.all(np.abs(fp8.decode_rows(c, s) - ref) <= 2.0 ** -4 * (np.abs(ref) + bound) + 2.0 ** -10 * scale + bound)
+    pad = np.zeros((M, s.shape[1] * 128))
+    for sign in (1, -1):
+        pad[:, :N] = np.abs(ref) + sign * bound
+        top = pad.reshape(M, -1, 128).max(2)
+        e = np.array([fp8.exponent_of(t) if t > 0 else -127 for t in top.ravel()]).reshape(top.shape) + 127
+        assert np.all(s <= e) if sign == 1 else np.all(s >= e)
+    assert bool((h[kq.fp8_act_bytes(N, M):] == 0xAA).all())
