@@ -48,6 +48,10 @@ namespace fp8 {
 namespace {
 
 constexpr int kMaxSplits = 8;
+// FUSED: the warps that encode, and the blocks of 128 values that they load together (two to a warp, kDeep
+// times), which is also the most that a CTA encodes.
+constexpr int kEncWarps = 12, kDeep = 4;
+constexpr int kEncRound = 2 * kEncWarps * kDeep;
 
 template <int BT, bool GATED, bool FUSED>
 struct Rows {
@@ -58,7 +62,11 @@ struct Rows {
   static constexpr uint32_t kSfOff = kProducts * kABytes + (FUSED ? 0 : kBBytes);   // scale atoms: weights, tokens
   static constexpr uint32_t kSfAtoms = kProducts + (FUSED ? 0 : 1);
   static constexpr uint32_t kStageBytes = kSfOff + (kSfAtoms > 2 ? 2048 : 1024);
-  static constexpr uint32_t kXBytes = FUSED ? 64 * 1024 : 0;               // encoded activations, at most
+  // k-tiles that a CTA can encode: kEncRound blocks of the fewest tokens of this tile, 64 KB at most.
+  // (128 BT bytes each, and their scale atoms: 4 k-tiles, or fewer at both ends of the share.)
+  static constexpr int kEncShare = kEncRound / (BT == 16 ? 1 : 17);
+  static constexpr int kMaxShare = FUSED ? (kEncShare < 512 / BT ? kEncShare : 512 / BT) : 1 << 30;
+  static constexpr uint32_t kXBytes = FUSED ? kMaxShare * kBBytes : 0;
   // Partials received in the exchange: [split][product][four tokens of the share][128 features] x
   // 16 bytes. Up to 16 tokens they have room of their own; beyond, they go over the ring once the
   // cluster's MMAs are done, which takes a cluster barrier more.
@@ -72,9 +80,6 @@ struct Rows {
   // accumulators 64 columns apart, then 3 scale sets of 16 columns
   static constexpr uint32_t kSfCol = kProducts * 64;
   static constexpr uint32_t kTmemCols = kSfCol + 48 <= 128 ? 128 : 256;
-  // k-tiles that a CTA can encode: 128 BT bytes each, and their scale atoms (4 k-tiles, or fewer
-  // at both ends of the share)
-  static constexpr int kMaxShare = FUSED ? static_cast<int>(kXBytes / kBBytes) : 1 << 30;
   static constexpr uint32_t smem(int share) {
     return 2048 + kRingBytes + (kOwnPart ? kPartBytes : 0) + (FUSED ? share * kBBytes + (share / 4 + 2) * 512 : 0);
   }
@@ -93,11 +98,12 @@ struct Rows {
 // epilogue warps call it together. A block of the 8-bit output is the CTA's 128 features of one
 // token: its largest value is found across the warps (`top` [4][16]), the codes are put together
 // in `tile` [T][128] and written 16 to a store; nothing is written if `bad` was set in any of them.
-template <int T, bool GATED>
+// BLOCKS: an 8-bit output is possible.
+template <int T, bool BLOCKS>
 __device__ __forceinline__ void store(const MmParams& p, const float* v, int token, int lim, int n0, int q, int lane,
                                       uint32_t* top, uint8_t* tile, const volatile uint32_t* bad) {
   const int n = n0 + 32 * q + lane;
-  if (GATED && p.out == 2) {
+  if (BLOCKS && p.out == 2) {
     asm volatile("bar.sync 1, 128;" ::: "memory");          // the last call's maxima and codes were read
     if (*bad) lim = 0;
     uint32_t m = 0;
@@ -139,38 +145,34 @@ __device__ __forceinline__ void store(const MmParams& p, const float* v, int tok
 
 // Encodes k-tiles kt0 .. kt0 + n - 1 of all tokens into shared memory: codes as [k-tile][BT rows
 // of 128 bytes] with the 128-byte swizzle, scale bytes as atoms. 16 lanes hold a block of 128
-// values, 8 each; kDeep blocks of each half-warp load together. `warp` of kEncWarps.
-constexpr int kEncWarps = 12, kDeep = 8;
-constexpr int kEncRound = 2 * kEncWarps * kDeep;           // blocks under way at once
+// values, 8 each, and all loads come first. `warp` of kEncWarps; n tokens <= kEncRound.
 template <int BT>
 __device__ __forceinline__ void encode_share(const MmParams& p, int tokens, int kt0, int n, uint8_t* codes, uint8_t* sf,
                                              int warp, int lane) {
   const int items = n * tokens, l = lane & 15;
-  for (int base = 2 * warp; base < items; base += kEncRound) {           // the same in both half-warps
-    uint4 u[kDeep];
+  uint4 u[kDeep];
 #pragma unroll
-    for (int j = 0; j < kDeep; ++j) {
-      const int item = base + (lane >> 4) + 2 * kEncWarps * j, i = item / tokens, t = item - i * tokens;
-      const int k = (kt0 + i) * kBlk + 8 * l;
-      u[j] = make_uint4(0, 0, 0, 0);
-      if (item < items && k < p.K)
-        u[j] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.xb) + t * p.ldx + k));
-    }
+  for (int j = 0; j < kDeep; ++j) {
+    const int item = 2 * (warp + kEncWarps * j) + (lane >> 4), i = item / tokens, t = item - i * tokens;
+    const int k = (kt0 + i) * kBlk + 8 * l;
+    u[j] = make_uint4(0, 0, 0, 0);
+    if (item < items && k < p.K)
+      u[j] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.xb) + t * p.ldx + k));
+  }
 #pragma unroll
-    for (int j = 0; j < kDeep; ++j) {
-      const int item = base + (lane >> 4) + 2 * kEncWarps * j, i = item / tokens, t = item - i * tokens;
-      if (base + 2 * kEncWarps * j >= items) break;                      // the same in both half-warps
-      float v[8];
-      unpack8(u[j], v);
-      const uint32_t byte = block_byte(v);
-      const float is = inv_scale(byte);
-      if (item < items) {
-        *reinterpret_cast<uint2*>(codes + i * (BT * 128) + t * 128 + 16 * ((l >> 1) ^ (t & 7)) + 8 * (l & 1)) =
-            make_uint2(e4m3x4(v[0] * is, v[1] * is, v[2] * is, v[3] * is),
-                       e4m3x4(v[4] * is, v[5] * is, v[6] * is, v[7] * is));
-        if (l == 0)
-          sf[512 * (((kt0 + i) >> 2) - (kt0 >> 2)) + 16 * (t & 31) + 4 * (t >> 5) + ((kt0 + i) & 3)] = static_cast<uint8_t>(byte);
-      }
+  for (int j = 0; j < kDeep; ++j) {
+    const int item = 2 * (warp + kEncWarps * j) + (lane >> 4), i = item / tokens, t = item - i * tokens;
+    if (2 * (warp + kEncWarps * j) >= items) break;                      // the same in both half-warps
+    float v[8];
+    unpack8(u[j], v);
+    const uint32_t byte = block_byte(v);
+    const float is = inv_scale(byte);
+    if (item < items) {
+      *reinterpret_cast<uint2*>(codes + i * (BT * 128) + t * 128 + 16 * ((l >> 1) ^ (t & 7)) + 8 * (l & 1)) =
+          make_uint2(e4m3x4(v[0] * is, v[1] * is, v[2] * is, v[3] * is),
+                     e4m3x4(v[4] * is, v[5] * is, v[6] * is, v[7] * is));
+      // (tokens of a 32-row quarter are 16 bytes apart; no more than 32 tokens are encoded here)
+      if (l == 0) sf[512 * (((kt0 + i) >> 2) - (kt0 >> 2)) + 16 * t + ((kt0 + i) & 3)] = static_cast<uint8_t>(byte);
     }
   }
 }
@@ -333,7 +335,7 @@ __global__ void __launch_bounds__(Rows<BT, ACT >= 0, FUSED>::kThreads) k_rows_mm
     }
   }
   if (epi) {
-    if (p.out == 2 && blockIdx.x == 0 && rank == 0 && threadIdx.x == 64) *p.oerr = 0u;
+    if (GATED && !FUSED && p.out == 2 && blockIdx.x == 0 && rank == 0 && threadIdx.x == 64) *p.oerr = 0u;
     ok = __all_sync(0xffffffffu, mbar_wait(acc_full, 0, p.err, KQ_DEV_ERR_TIMEOUT_ACC, p.wait_ns));
     if (!ok) *bad = 1u;
     tc_fence_after();
@@ -390,7 +392,7 @@ __global__ void __launch_bounds__(Rows<BT, ACT >= 0, FUSED>::kThreads) k_rows_mm
               v[j][4 * f] += w.x; v[j][4 * f + 1] += w.y; v[j][4 * f + 2] += w.z; v[j][4 * f + 3] += w.w;
             }
         if (GATED) gate<ACT, 4 * F>(p.out, v[0], v[C::kProducts - 1], v[0]);
-        store<4 * F, GATED>(p, v[0], 4 * four, ok ? min(min(4 * F, 4 * (qe - four)), tokens - 4 * four) : 0, n0, q, lane, top, tile, bad);
+        store<4 * F, GATED && !FUSED>(p, v[0], 4 * four, ok ? min(min(4 * F, 4 * (qe - four)), tokens - 4 * four) : 0, n0, q, lane, top, tile, bad);
       }
     }
   } else if (epi) {
@@ -405,7 +407,7 @@ __global__ void __launch_bounds__(Rows<BT, ACT >= 0, FUSED>::kThreads) k_rows_mm
 #pragma unroll
         for (int t = 0; t < 16; ++t) v[j][t] = __uint_as_float(r[j][t]);
       if (GATED) gate<ACT, 16>(p.out, v[0], v[C::kProducts - 1], v[0]);
-      store<16, GATED>(p, v[0], c, ok ? min(16, tokens - c) : 0, n0, q, lane, top, tile, bad);
+      store<16, GATED && !FUSED>(p, v[0], c, ok ? min(16, tokens - c) : 0, n0, q, lane, top, tile, bad);
     }
   }
   tc_fence_before();
@@ -482,8 +484,8 @@ bool try_rows(const MmParams& p, const Device& d, cudaStream_t st, cudaError_t* 
   const int splits = rows_splits<BT, ACT, FUSED>(cdiv(p.N, 128), kt, d.sms, d.device);
   // Encoding on the way in adds 0.8 us to the product for 4 blocks of a CTA, 1.3 for 32, 1.7 for 64
   // and 2.5 for 128 (512 -> 512, 1 to 32 tokens), a kernel of its own 1.6 and a launch, which costs
-  // the host more than 2 us: half a round of blocks at most.
-  if (FUSED && (cdiv(kt, splits) > C::kMaxShare || cdiv(kt, splits) * p.M > kEncRound / 2)) return false;
+  // the host more than 2 us: one round of blocks at most.
+  if (FUSED && (cdiv(kt, splits) > C::kMaxShare || cdiv(kt, splits) * p.M > kEncRound)) return false;
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = rows_config<BT, ACT >= 0, FUSED>(p, splits, attr, st);
   *e = cudaLaunchKernelEx(&cfg, fn, p);
