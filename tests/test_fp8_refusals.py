@@ -140,3 +140,26 @@ def test_debug_wait_timeout():
     assert t(o=OK, on=BIG, Y=None) == 1                                 # not gated
     assert t(d=d, o=OK, on=BIG) == 1 and t(d=d, o=OK2, on=BIG, Y=None) == 1 and t(d=d, o=OK, on=64, Y=None) == 5
     assert t(d=d, o=OK, on=BIG, X=OK, ldx=64, Y=None) == 1
+
+
+def test_sizes_past_32_bits():
+    """Sizes that the C ABI's 32-bit fields cannot hold are refused, not cut to their low bits."""
+    far = (1 << 32) + 64
+    for K, N in ((far, 64), (64, far), (-far, 64), (1 << 31, 64)):
+        with pytest.raises(ValueError, match="32 bits"):
+            kq.Fp8Layer(K, N)
+    g, d = L(64, 96, True), L(96, 64)
+    for M in (far, 1 << 31, 1 - far):
+        assert kq.fp8_act_bytes(64, M) == 0 and kq.fp8_act_bytes(M, 4) == 0 and kq.fp8_ffn_bytes(g, d, M) == 0
+    act, Y = torch.zeros(1 << 16, dtype=torch.uint8), torch.empty(far, 64, device="meta")
+    wide, tall = (torch.empty(n, k, dtype=torch.bfloat16, device="meta") for n, k in ((1, far), (far, 64)))
+    with pytest.raises(ValueError, match=f"needs {64 * far}"):
+        kq.fp8_act_pack(64, act, act, far, act)
+    calls = [lambda: kq.fp8_act_unpack(64, act, far),
+             lambda: kq.fp8_act_unpack(far, act, 4), lambda: kq.fp8_gemm(L(), act, act, far, Y),
+             lambda: kq.fp8_gated_act(g, act, act, far, act), lambda: kq.fp8_quantize_act(wide, act),
+             lambda: kq.fp8_quantize_act(tall, act), lambda: kq.fp8_rmsnorm_act(tall, torch.ones(64), 1e-6, act),
+             lambda: kq.fp8_linear(L(), act, tall, Y, act), lambda: kq.fp8_ffn(g, act, d, act, tall, None, 1e-6, Y, act)]
+    for f in calls:
+        with pytest.raises(ValueError, match="32 bits"):
+            f()

@@ -397,6 +397,12 @@ def debug_wait_timeout(layer: Layer, act, M: int, limit_us: int, stream=None) ->
 
 
 # ---------------------------------------------------------------- 8-bit operators --------
+def _fits(size: int, name: str) -> None:
+    """ctypes would pass the low 32 bits of a size to the C ABI without a word."""
+    if not -1 << 31 <= size < 1 << 31:
+        raise ValueError(f"{name} = {size} is past 32 bits")
+
+
 class Fp8Layer:
     """One 8-bit linear layer (the C ``kq_fp8_desc``): E4M3 codes with a power-of-two scale for
     each token and 128 features, and for each 128 x 128 piece of a weight. ``gated``: two
@@ -404,6 +410,7 @@ class Fp8Layer:
 
     def __init__(self, K: int, N: int, gated: bool = False, activation: str = "silu"):
         self.K, self.N, self.gated, self.activation = int(K), int(N), bool(gated), activation
+        _fits(self.K, "K"), _fits(self.N, "N")
         self._desc = _Fp8Desc(K=self.K, N=self.N, gated=int(self.gated), activation=_ACTIVATION[activation])
         self._ref = ctypes.byref(self._desc)
         self._weights_bytes = fp8_weights_bytes(self)
@@ -492,11 +499,13 @@ def fp8_weights_bytes(layer: Fp8Layer) -> int:
 
 @functools.lru_cache(maxsize=4096)
 def fp8_act_bytes(K: int, M: int) -> int:
-    return int(lib.kq_fp8_act_bytes(int(K), int(M)))
+    """0 for sizes that no call takes."""
+    return int(lib.kq_fp8_act_bytes(int(K), int(M))) if 0 < min(K, M) and max(K, M) < 1 << 31 else 0
 
 
 def fp8_ffn_bytes(gated: Fp8Layer, down: Fp8Layer, M: int) -> int:
-    return int(lib.kq_fp8_ffn_bytes(gated.desc, down.desc, int(M)))
+    """0 for sizes that no call takes."""
+    return int(lib.kq_fp8_ffn_bytes(gated.desc, down.desc, int(M))) if 0 < M < 1 << 31 else 0
 
 
 def _fp8_pair(layer: Fp8Layer, up, name: str) -> None:
@@ -559,7 +568,10 @@ def fp8_weights_unpack(layer: Fp8Layer, weights, codes=None, scales=None, up_cod
 
 
 def _fp8_act(act, K: int, M: int, name: str = "act"):
-    return _flat(act, _names().u8, fp8_act_bytes(K, M), name)
+    n = fp8_act_bytes(K, M)
+    if not n:
+        _fits(K, "K"), _fits(M, "M")
+    return _flat(act, _names().u8, n, name)
 
 
 def fp8_quantize_act(X, act, stream=None) -> None:
@@ -664,6 +676,7 @@ def fp8_ffn(gated: Fp8Layer, gated_weights, down: Fp8Layer, down_weights, X, gam
     _fp8_weights(down, down_weights)
     if not gated.gated or down.gated or down.K != gated.N or M < 1:
         raise ValueError("fp8_ffn takes a gated layer and a plain one with K equal to its N, and M >= 1")
+    _fits(M, "M")
     _flat(ws, _names().u8, fp8_act_bytes(gated.K, M) + fp8_act_bytes(gated.N, M), "ws")
     ldx = _rows(X, _names().bf16, None, gated.K, "X")
     if gamma is None and residual is not None:
