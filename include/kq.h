@@ -356,7 +356,7 @@ kq_status kq_debug_wait_timeout(const kq_layer_desc *desc, void *act, int32_t M,
  * accumulate in fp32.
  *
  * Matrices are row-major; ldx, ldr, ldy are row pitches in elements (at least the width,
- * rows a multiple of 16 bytes apart). K % 32 == 0, N % 16 == 0, M >= 1. Conventions for
+ * rows a multiple of 16 bytes apart). K % 32 == 0, N % 16 == 0, both at most 2^28, M >= 1. Conventions for
  * ownership, streams, errors and alignment are those at the top of this file. Calls that
  * may run at the same time need workspaces of their own.
  * ------------------------------------------------------------------------------- */
@@ -365,8 +365,8 @@ typedef enum { KQ_ACT_SILU = 0, KQ_ACT_GELU = 1 } kq_activation;
 /* One 8-bit layer. gated == 0: Y = X W, W [K, N]. gated == 1: two matrices of that shape
  * and Y = act(X Wgate) * (X Wup), act SiLU  z / (1 + e^-z)  or GELU in its erf form. */
 typedef struct {
-  int32_t K;             /* input features, K % 32 == 0 */
-  int32_t N;             /* output features, N % 16 == 0 */
+  int32_t K;             /* input features, K % 32 == 0, at most 2^28 */
+  int32_t N;             /* output features, N % 16 == 0, at most 2^28 */
   int32_t gated;         /* 0 or 1 */
   int32_t activation;    /* kq_activation, used when gated */
 } kq_fp8_desc;

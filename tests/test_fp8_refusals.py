@@ -163,3 +163,12 @@ def test_sizes_past_32_bits():
     for f in calls:
         with pytest.raises(ValueError, match="32 bits"):
             f()
+
+
+def test_widest_layers():
+    top = 1 << 28
+    assert kq.fp8_weights_bytes(L(top, 16)) > top * 16 and kq.fp8_weights_bytes(L(32, top)) > top * 32
+    assert kq.fp8_weights_bytes(L(top + 32, 16)) == 0 and kq.fp8_weights_bytes(L(32, top + 16)) == 0
+    assert kq.fp8_act_bytes(top, 1) > top and kq.fp8_act_bytes(top + 32, 1) == 0
+    assert quant(K=top + 32, ldx=top + 32) == 2
+    assert lib.kq_fp8_gemm(L(32, top + 16).desc, OK, OK2, 1, OK, top + 16, 0, None) == 2

@@ -738,3 +738,34 @@ def test_8bit_output_of_few_tokens(cuda_device, M, K, N, kind):
         e = np.array([fp8.exponent_of(t) if t > 0 else -127 for t in top.ravel()]).reshape(top.shape) + 127
         assert np.all(s <= e) if sign == 1 else np.all(s >= e)
     assert bool((h[kq.fp8_act_bytes(N, M):] == 0xAA).all())
+
+
+def test_more_outputs_than_65535_blocks(cuda_device):
+    """8.4 million outputs, 2049 copies of the same 4096: each copy's codes, scales and outputs are alike."""
+    import torch
+    import w4a4_post_quantization_token_b200 as kq
+    K, n, copies = 32, 4096, 2049
+    W = weight(K, n, 5).cuda()
+    small, big = kq.Fp8Layer(K, n), kq.Fp8Layer(K, n * copies)
+    ws, wb = buf(kq.fp8_weights_bytes(small)), buf(kq.fp8_weights_bytes(big))
+    kq.fp8_prepare_weights(small, W, ws)
+    kq.fp8_prepare_weights(big, W.repeat(1, copies), wb)
+    cs, ss, cb, sb = buf(n * K), buf(n // 128), buf(n * K * copies), buf(n // 128 * copies)
+    kq.fp8_weights_unpack(small, ws, cs, ss)
+    kq.fp8_weights_unpack(big, wb, cb, sb)
+    assert torch.equal(cb.view(copies, -1), cs.expand(copies, -1)) and torch.equal(sb.view(copies, -1), ss.expand(copies, -1))
+    for M in (1, 66):
+        X, act = tokens(M, K, 6).cuda(), buf(kq.fp8_act_bytes(K, M))
+        Ys, Yb = (torch.zeros(M, w, dtype=torch.bfloat16, device="cuda") for w in (n, n * copies))
+        kq.fp8_linear(small, ws, X, Ys, act, kq.OUT_BF16)
+        kq.fp8_linear(big, wb, X, Yb, act, kq.OUT_BF16)
+        assert kq.fp8_last_device_error(act) == 0
+        assert torch.equal(Yb.view(M, copies, n), Ys[:, None].expand(M, copies, n)) and bool((Ys != 0).any())
+
+
+def test_rows_of_more_than_2_28_features_are_refused(cuda_device):
+    import torch
+    import w4a4_post_quantization_token_b200 as kq
+    K = (1 << 28) + 32
+    with pytest.raises(kq.KQError):
+        kq.fp8_quantize_act(torch.empty(1, K, dtype=torch.bfloat16, device="cuda"), buf(1 << 20))

@@ -26,6 +26,9 @@ namespace fp8 {
 
 constexpr int kBlk = 128;                    // elements per scale along K; bytes per k-tile row
 constexpr int kNormMaxK = 32768;             // the norm keeps a row in registers
+// Features of a layer, in or out: grids and 32-bit indices hold them, and a product over so many
+// inputs (2^21 k-tiles, 0.3 us each) ends well within the 2 s that its epilogue waits.
+constexpr int kMaxWidth = 1 << 28;
 
 __host__ __device__ constexpr int64_t katoms(int64_t K) { return cdiv(K, 4 * kBlk); }
 

@@ -13,14 +13,15 @@ namespace {
 
 kq_status check_width(int32_t K) {
   if (K <= 0) return KQ_ERR_INVALID_ARG;
-  return K % 32 == 0 ? KQ_OK : KQ_ERR_UNSUPPORTED_SHAPE;
+  return K % 32 == 0 && K <= fp8::kMaxWidth ? KQ_OK : KQ_ERR_UNSUPPORTED_SHAPE;
 }
 
 kq_status check_fp8(const kq_fp8_desc* d) {
   if (!d || d->K <= 0 || d->N <= 0) return KQ_ERR_INVALID_ARG;
   if (d->gated != 0 && d->gated != 1) return KQ_ERR_INVALID_ARG;
   if (d->activation != KQ_ACT_SILU && d->activation != KQ_ACT_GELU) return KQ_ERR_INVALID_ARG;
-  if (d->K % 32 != 0 || d->N % 16 != 0) return KQ_ERR_UNSUPPORTED_SHAPE;
+  if (d->K % 32 != 0 || d->N % 16 != 0 || d->K > fp8::kMaxWidth || d->N > fp8::kMaxWidth)
+    return KQ_ERR_UNSUPPORTED_SHAPE;
   return KQ_OK;
 }
 

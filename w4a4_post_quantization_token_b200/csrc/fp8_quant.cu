@@ -212,13 +212,15 @@ cudaError_t launch_norm_c(const NormParams& p, int res_kind, dim3 grid, int T, c
   return launch_behind(res_kind == 0 ? k_norm<C, 0> : res_kind == 1 ? k_norm<C, 1> : k_norm<C, 2>, grid, dim3(T), st, p);
 }
 
-// One CTA per 128 (outputs) x 128 (inputs) piece of W [K, N]: transposed to K-major codes.
+// One CTA per 128 (outputs) x 128 (inputs) piece of W [K, N]: transposed to K-major codes. (The pieces
+// are one grid dimension: a second one ends at 65535.)
 __global__ void __launch_bounds__(256) k_weight_quant(const uint16_t* __restrict__ W, int K, int N,
                                                       uint8_t* __restrict__ codes, uint8_t* __restrict__ sf,
                                                       int64_t ka) {
   __shared__ uint16_t tile[128][130];                     // [k][n]
   __shared__ uint32_t top[8];
-  const int k0 = blockIdx.x * 128, n0 = blockIdx.y * 128;
+  const uint32_t kb = static_cast<uint32_t>(cdiv(K, 128)), bk = blockIdx.x % kb;
+  const int k0 = static_cast<int>(bk) * 128, n0 = static_cast<int>(blockIdx.x / kb) * 128;
   uint32_t a = 0;
   for (int i = threadIdx.x; i < 128 * 128; i += 256) {
     const int k = i >> 7, n = i & 127;
@@ -242,7 +244,7 @@ __global__ void __launch_bounds__(256) k_weight_quant(const uint16_t* __restrict
     for (int j = 0; j < 4; ++j) v[j] = __uint_as_float(static_cast<uint32_t>(tile[k + j][n]) << 16) * is;
     *reinterpret_cast<uint32_t*>(codes + static_cast<size_t>(n0 + n) * K + k0 + k) = e4m3x4(v[0], v[1], v[2], v[3]);
   }
-  if (threadIdx.x < 128) sf[sf_offset(n0 + threadIdx.x, blockIdx.x, ka)] = static_cast<uint8_t>(byte);
+  if (threadIdx.x < 128) sf[sf_offset(n0 + threadIdx.x, bk, ka)] = static_cast<uint8_t>(byte);
 }
 
 // Canonical weight scales [cdiv(N, 128), cdiv(K, 128)] <-> atoms (every row of a block alike).
@@ -334,8 +336,7 @@ cudaError_t launch_rows(const NormParams& p, bool norm, int res_kind, cudaStream
 }
 
 cudaError_t launch_weight_quant(const void* W, int K, int N, uint8_t* codes, uint8_t* sf, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>(cdiv(K, 128)), static_cast<unsigned>(cdiv(N, 128)));
-  k_weight_quant<<<grid, 256, 0, st>>>(static_cast<const uint16_t*>(W), K, N, codes, sf, katoms(K));
+  k_weight_quant<<<static_cast<unsigned>(cdiv(K, 128) * cdiv(N, 128)), 256, 0, st>>>(static_cast<const uint16_t*>(W), K, N, codes, sf, katoms(K));
   return cudaGetLastError();
 }
 
