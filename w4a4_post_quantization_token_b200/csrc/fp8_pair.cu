@@ -17,6 +17,9 @@
 // and 192 .. 447): the epilogue reads the shared 64 columns first, and the next tile's MMAs start
 // when those are out, some 1800 cycles after the last MMA.
 //
+// LONG: fp32 outputs of more k-tiles than sum_tiles. A tile's pieces take the two accumulators in turn, as
+// tiles do, and the epilogue adds them in registers.
+//
 // A wait that runs out ends the kernel as in k_rows_mm: the MMA issuer waits for its MMAs and for the
 // loads of both CTAs that are under way, an epilogue warp stores nothing from the tile whose
 // accumulators did not come, frees none and leaves.
@@ -165,11 +168,12 @@ __device__ __forceinline__ bool put_gated(const MmParams& p, const float (&v)[64
 }
 
 // ACT: -1 plain, 0 SiLU-gated, 1 GELU-gated. SPLIT: K is shared by the 2 or 4 pairs of a cluster.
-template <int BN, int ACT, bool SPLIT>
+template <int BN, int ACT, bool SPLIT, bool LONG>
 __global__ void __launch_bounds__(Pair<BN>::kThreads, 1) k_mm_pair(const __grid_constant__ MmParams p) {
   using C = Pair<BN>;
   constexpr bool GATED = ACT >= 0;
   constexpr int kBN = GATED ? BN / 2 : BN;                           // output columns of a tile
+  constexpr int kSum = sum_tiles(GATED);
   static_assert(!GATED || (BN == 256 && !SPLIT), "an 8-bit block is the 128 outputs of a gated tile");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(align_up(reinterpret_cast<uintptr_t>(smem_raw), 1024));
@@ -209,6 +213,45 @@ __global__ void __launch_bounds__(Pair<BN>::kThreads, 1) k_mm_pair(const __grid_
   cluster_sync();                                                    // both CTAs' barriers exist
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+
+  // Each warp of both CTAs frees an accumulator when it has read its columns (16 arrivals). Shared
+  // columns are the second half's of accumulator 0 and the first half's of 1: their owner frees
+  // the other accumulator after reading them, and its own after reading the rest; the first
+  // half's share of accumulator 1's first turn is free from the start.
+  const uint32_t free0 = mapa_shared(smem_u32(&acc_free[0]), lead);
+  auto release = [&](int b) {
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_cluster(free0 + 8u * static_cast<uint32_t>(b));
+  };
+  // LONG: the sums of a tile, in the order of its pieces. v: the half's columns (gated: 64 of the gate,
+  // then the same of up), the shared ones read first. False if a piece did not come.
+  auto sum_tile = [&](int& local, float (&v)[BN / 2]) {
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    for (int k0 = kt0; k0 < kt1; k0 += kSum, ++local) {
+      const int buf = local & 1;
+      const bool owner = half != buf, more = k0 > kt0;
+      if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (local >> 1) & 1, p.err, KQ_DEV_ERR_TIMEOUT_ACC, p.wait_ns)))
+        return false;
+      tc_fence_after();
+      const uint32_t tb = tmem + static_cast<uint32_t>(buf) * C::kAccStride + (static_cast<uint32_t>(32 * q) << 16);
+      if (!C::kShared) {
+        add_columns<BN / 2>(tb + BN / 2 * half, more, v);
+        release(buf);
+      } else {
+        // two runs of 64 columns: gate and up, or the halves of this half
+        const uint32_t c0 = tb + (GATED ? 64 : 128) * half, c1 = c0 + (GATED ? 128 : 64);
+        const bool swap = buf == 0 && (GATED || half == 1);
+        if (swap) add_columns<64>(c1, more, v + 64);
+        else add_columns<64>(c0, more, v);
+        if (owner) release(buf ^ 1);
+        if (swap) add_columns<64>(c0, more, v);
+        else add_columns<64>(c1, more, v + 64);
+        if (owner) release(buf);
+      }
+    }
+    return true;
+  };
 
   if (warp == 0 || warp == 10) {
     const bool tokens = warp == 0;
@@ -271,52 +314,55 @@ __global__ void __launch_bounds__(Pair<BN>::kThreads, 1) k_mm_pair(const __grid_
       int s = 0, local = 0, set = C::kSets - 1;
       uint32_t ph = 0;
       const int64_t per = kt1 - kt0;
-      int64_t stop = -1;                                             // k-tiles taken when a wait ran out
+      int64_t before = 0, stop = -1;                                 // k-tiles of earlier tiles; taken when a wait ran out
       grid_dep_wait();
-      for (int tile = first; tile < T && stop < 0; tile += step, ++local) {
-        const int buf = local & 1;
-        const int since = C::kShared && buf ? local - 1 : local - 2;  // tiles since acc_free[buf]'s first phase
-        if (since >= 0 && !mbar_wait_cluster(&acc_free[buf], (since >> 1) & 1, p.err, KQ_DEV_ERR_TIMEOUT_ACC, p.wait_ns)) {
-          stop = local * per;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d = tmem + static_cast<uint32_t>(buf) * C::kAccStride;
+      for (int tile = first; tile < T && stop < 0; tile += step, before += per) {
         uint32_t shift = 0;                                          // a tile may start in mid-atom
         if (BN % 128 != 0) {
           int mt, nt;
           pair_tile(tile, MT, NT, mt, nt);
           shift = static_cast<uint32_t>(nt * BN % 128) / 32u;
         }
-        uint32_t acc = 0;
-        for (int kt = kt0; kt < kt1; ++kt) {
-          if (!mbar_wait(&full[s], ph, p.err, KQ_DEV_ERR_TIMEOUT_FULL, p.wait_ns)) {
-            stop = local * per + kt - kt0;
+        for (int k0 = kt0, k1; k0 < kt1 && stop < 0; k0 = k1, ++local) {
+          k1 = LONG ? min(k0 + kSum, kt1) : kt1;                       // a piece; not LONG: the tile
+          const int buf = local & 1;
+          const int since = C::kShared && buf ? local - 1 : local - 2;  // pieces since acc_free[buf]'s first phase
+          if (since >= 0 && !mbar_wait_cluster(&acc_free[buf], (since >> 1) & 1, p.err, KQ_DEV_ERR_TIMEOUT_ACC, p.wait_ns)) {
+            stop = before + k0 - kt0;
             break;
           }
           tc_fence_after();
-          const uint32_t id = static_cast<uint32_t>(kt) & 3u;
-          if (id == 0 || (SPLIT && kt == kt0)) {
-            set = set + 1 == C::kSets ? 0 : set + 1;
-            f = tmem + C::kSfCol + C::kSfSet * set;
-            scale_cp_if<true>(one, f, sd);
-            scale_cp_if<true>(one, f + 4, sd + 32);
-            if (C::kWAtoms > 1) scale_cp_if<true>(one, f + 8, sd + 64);
-          }
-          const uint32_t idesc = idesc_mxf8(256, BN, 0) | (id << 4) | (id << 29);
-          const uint32_t fa = f | (id << 30);
-          // all four K steps of 32, the last k-tile's too: what lies past K was filled with zeros
+          const uint32_t d = tmem + static_cast<uint32_t>(buf) * C::kAccStride;
+          uint32_t acc = 0;
+          for (int kt = k0; kt < k1; ++kt) {
+            if (!mbar_wait(&full[s], ph, p.err, KQ_DEV_ERR_TIMEOUT_FULL, p.wait_ns)) {
+              stop = before + kt - kt0;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t id = static_cast<uint32_t>(kt) & 3u;
+            if (id == 0 || (SPLIT && kt == kt0)) {
+              set = set + 1 == C::kSets ? 0 : set + 1;
+              f = tmem + C::kSfCol + C::kSfSet * set;
+              scale_cp_if<true>(one, f, sd);
+              scale_cp_if<true>(one, f + 4, sd + 32);
+              if (C::kWAtoms > 1) scale_cp_if<true>(one, f + 8, sd + 64);
+            }
+            const uint32_t idesc = idesc_mxf8(256, BN, 0) | (id << 4) | (id << 29);
+            const uint32_t fa = f | (id << 30);
+            // all four K steps of 32, the last k-tile's too: what lies past K was filled with zeros
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_mxf8_if<true>(one, d, ad0 + so + 2 * kk, bd0 + so + 2 * kk, idesc, fa, fa + 4 + shift, kk == 0 ? acc : 1u);
-          commit_if<true>(one, bar, both);
-          acc = 1;
-          so += C::kStageBytes >> 4;
-          sd += C::kSfBytes >> 4;
-          bar += 8;
-          if (++s == C::kStages) { s = 0; ph ^= 1u; so = 0; sd = sd0; bar = smem_u32(empty); }
+            for (int kk = 0; kk < 4; ++kk)
+              mma_mxf8_if<true>(one, d, ad0 + so + 2 * kk, bd0 + so + 2 * kk, idesc, fa, fa + 4 + shift, kk == 0 ? acc : 1u);
+            commit_if<true>(one, bar, both);
+            acc = 1;
+            so += C::kStageBytes >> 4;
+            sd += C::kSfBytes >> 4;
+            bar += 8;
+            if (++s == C::kStages) { s = 0; ph ^= 1u; so = 0; sd = sd0; bar = smem_u32(empty); }
+          }
+          if (stop < 0) commit_if<true>(one, smem_u32(&acc_full[buf]), both);
         }
-        if (stop < 0) commit_if<true>(one, smem_u32(&acc_full[buf]), both);
       }
       if (stop >= 0) {
         // the barriers count the loads of both CTAs; the peer leaves after the cluster barrier below
@@ -329,29 +375,37 @@ __global__ void __launch_bounds__(Pair<BN>::kThreads, 1) k_mm_pair(const __grid_
     grid_dep_wait();
     const int q = warp & 3, half = (warp - 2) >> 2;
     uint8_t* stg = smem + C::kStgOff + static_cast<uint32_t>(warp - 2) * C::kStgBytes;
-    const uint32_t free0 = mapa_shared(smem_u32(&acc_free[0]), lead);
     if (GATED && p.out == 2 && blockIdx.x == 0 && threadIdx.x == 64) *p.oerr = 0u;
-    // Each warp of both CTAs frees an accumulator when it has read its columns (16 arrivals). Shared
-    // columns are the second half's of accumulator 0 and the first half's of 1: their owner frees
-    // the other accumulator after reading them, and its own after reading the rest; the first
-    // half's share of accumulator 1's first turn is free from the start.
-    if (!SPLIT && C::kShared && half == 0 && lane == 0) mbar_arrive_cluster(free0 + 8);
+    if ((!SPLIT || LONG) && C::kShared && half == 0 && lane == 0) mbar_arrive_cluster(free0 + 8);
     int local = 0;
     for (int tile = SPLIT ? T : first; tile < T; tile += step, ++local) {
       int mt, nt;
       pair_tile(tile, MT, NT, mt, nt);
       const int m0 = mt * 256 + 128 * static_cast<int>(rank) + 32 * q;
+      if constexpr (LONG) {
+        float v[BN / 2];
+        if (!sum_tile(local, v)) break;
+        --local;                                                     // it counted the tile's last piece
+#pragma unroll
+        for (int c = 0; c < kBN / 2; c += 32) {
+          float w[32];
+          if constexpr (GATED) {
+            gate<ACT, 32>(0, v + c, v + 64 + c, w);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[i] = v[c + i];
+          }
+          const int n0 = nt * kBN + kBN / 2 * half + c;
+          if (n0 < p.N) put_values(p, w, stg, n0, m0, true, lane);
+        }
+        continue;
+      }
       const int buf = local & 1;
       const bool owner = half != buf;
       bool ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (local >> 1) & 1, p.err, KQ_DEV_ERR_TIMEOUT_ACC, p.wait_ns));
       if (!GATED && !ok) break;
       tc_fence_after();
       const uint32_t tb = tmem + static_cast<uint32_t>(buf) * C::kAccStride + (static_cast<uint32_t>(32 * q) << 16);
-      auto release = [&](int b) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0 && ok) mbar_arrive_cluster(free0 + 8u * static_cast<uint32_t>(b));
-      };
       if (!GATED) {
         // chunks of 64 (or 32) columns; the shared ones first: 192 .. 255 in the second half of
         // accumulator 0, 0 .. 63 in the first of accumulator 1
@@ -384,13 +438,13 @@ __global__ void __launch_bounds__(Pair<BN>::kThreads, 1) k_mm_pair(const __grid_
 #pragma unroll
           for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i >> 5][i & 31]);
         }
-        if (owner) release(buf ^ 1);
+        if (owner && ok) release(buf ^ 1);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t r[32];
           tmem_ld_32x32b_x32((buf == 0 ? g0 : u0) + 32 * c, r);
           tmem_ld_wait();
-          if (owner && c == 1) release(buf);
+          if (owner && ok && c == 1) release(buf);
           float g[32], u[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
@@ -412,9 +466,15 @@ __global__ void __launch_bounds__(Pair<BN>::kThreads, 1) k_mm_pair(const __grid_
     const bool epi = warp >= 2 && warp < 10;
     const int q = warp & 3, nq = 4 / splits;
     bool ok = true;
+    [[maybe_unused]] float sum[BN / 2];                              // LONG
     if (epi) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[0], 0, p.err, KQ_DEV_ERR_TIMEOUT_ACC, p.wait_ns));
-      tc_fence_after();
+      if constexpr (LONG) {
+        int local = 0;
+        ok = sum_tile(local, sum);
+      } else {
+        ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[0], 0, p.err, KQ_DEV_ERR_TIMEOUT_ACC, p.wait_ns));
+        tc_fence_after();
+      }
     }
     __syncwarp();
     cluster_sync();                                                  // every CTA's ring has been consumed
@@ -423,14 +483,20 @@ __global__ void __launch_bounds__(Pair<BN>::kThreads, 1) k_mm_pair(const __grid_
       const uint32_t at = mapa_shared(smem_u32(ring), 2u * static_cast<uint32_t>(dest) + rank) +
                           512u * static_cast<uint32_t>((split * nq + q - dest * nq) * (BN / 4)) +
                           16u * static_cast<uint32_t>(lane);
-#pragma unroll 1
-      for (int c = BN / 2 * half; c < BN / 2 * (half + 1); c += 32) {
+#pragma unroll(LONG ? BN / 64 : 1)
+      for (int c = 0; c < BN / 2; c += 32) {
         uint32_t r[32];
-        tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(32 * q) << 16) + c, r);
-        tmem_ld_wait();
+        if constexpr (LONG) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(sum[c + i]);
+        } else {
+          tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(32 * q) << 16) + BN / 2 * half + c, r);
+          tmem_ld_wait();
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          st_shared_cluster_v4(at + 512u * static_cast<uint32_t>(c / 4 + j), r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+          st_shared_cluster_v4(at + 512u * static_cast<uint32_t>((BN / 2 * half + c) / 4 + j), r[4 * j], r[4 * j + 1],
+                               r[4 * j + 2], r[4 * j + 3]);
       }
     }
     if (!ok && lane < 2 * splits) st_shared_cluster_u32(mapa_shared(smem_u32(const_cast<uint32_t*>(bad)), lane), 1u);
@@ -489,7 +555,8 @@ cudaLaunchConfig_t pair_config(int64_t clusters, int splits, cudaLaunchAttribute
 
 template <int BN, int ACT, bool SPLIT>
 cudaError_t launch_pair_kernel(const MmParams& p, int sms, cudaStream_t st) {
-  auto fn = k_mm_pair<BN, ACT, SPLIT>;
+  auto fn = k_mm_pair<BN, ACT, SPLIT, false>;
+  if (p.out == 0 && cdiv(cdiv(p.K, kBlk), SPLIT ? p.splits : 1) > sum_tiles(ACT >= 0)) fn = k_mm_pair<BN, ACT, SPLIT, true>;
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(Pair<BN>::kSmem));
   if (e != cudaSuccess) return e;
   const int64_t tiles = cdiv(p.M, 256) * cdiv(p.N, ACT >= 0 ? BN / 2 : BN);
@@ -508,7 +575,7 @@ int64_t max_pair_clusters(int splits, int device) {
   std::atomic<int>& k = known[device][splits / 4];
   int n = k.load(std::memory_order_relaxed);
   if (n > 0) return n - 1;
-  auto fn = k_mm_pair<BN, -1, true>;
+  auto fn = k_mm_pair<BN, -1, true, false>;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = pair_config<BN, -1, true>(1, splits, attr, nullptr);
   cfg.numAttrs = 1;

@@ -17,6 +17,9 @@
 //             product, a commit that frees the stage.
 //   warps 2-5 epilogue: thread = output feature; a warp writes 32 neighbouring features of one
 //             token at a time.
+// LONG: fp32 outputs of more k-tiles than sum_tiles. After each piece the issuer waits until the epilogue
+// has added the accumulators to its sums in registers; the ring goes on filling meanwhile.
+//
 // A wait that runs out ends the kernel without an output: the MMA issuer does not commit the
 // accumulators, waits for its MMAs and for the loads under way, and the epilogue's own wait for the
 // accumulators runs out too. It stores nothing then, and neither does a CTA that lacks its sums.
@@ -178,17 +181,20 @@ __device__ __forceinline__ void encode_share(const MmParams& p, int tokens, int 
 }
 
 // ACT: -1 plain, 0 SiLU-gated, 1 GELU-gated
-template <int BT, int ACT, bool FUSED>
+template <int BT, int ACT, bool FUSED, bool LONG>
 __global__ void __launch_bounds__(Rows<BT, ACT >= 0, FUSED>::kThreads) k_rows_mm(const __grid_constant__ MmParams p) {
   constexpr bool GATED = ACT >= 0;
+  constexpr int kSum = sum_tiles(GATED);
   using C = Rows<BT, GATED, FUSED>;
+  static_assert(!LONG || !FUSED, "a CTA encodes fewer k-tiles");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(align_up(reinterpret_cast<uintptr_t>(smem_raw), 1024));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem);
   uint64_t* empty = full + C::kStages;
   uint64_t* acc_full = empty + C::kStages;
   uint64_t* x_ready = acc_full + 1;
-  uint64_t* mma_done = x_ready + 1;                                      // after a wait ran out
+  uint64_t* acc_free = x_ready + 1;                                      // LONG
+  uint64_t* mma_done = acc_free + 1;                                     // after a wait ran out
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile uint32_t* bad = tmem_slot + 1;                                // sums of this CTA's outputs are missing
   uint32_t* top = reinterpret_cast<uint32_t*>(smem + 512);               // [4 warps][16 tokens]
@@ -207,6 +213,7 @@ __global__ void __launch_bounds__(Rows<BT, ACT >= 0, FUSED>::kThreads) k_rows_mm
     for (int s = 0; s < C::kStages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
     mbar_init(acc_full, 1);
     mbar_init(x_ready, 32 * kEncWarps);
+    mbar_init(acc_free, 4);
     mbar_init(mma_done, 1);
     *bad = 0;
     fence_mbar_init();
@@ -284,6 +291,12 @@ __global__ void __launch_bounds__(Rows<BT, ACT >= 0, FUSED>::kThreads) k_rows_mm
     grid_dep_wait();
     bool ok = !FUSED || mbar_wait(x_ready, 0, p.err, KQ_DEV_ERR_TIMEOUT_FULL, p.wait_ns);
     for (; i < n_kt && ok; ++i) {
+      if (LONG && i > 0 && i % kSum == 0) {
+        commit_if<false>(one, smem_u32(acc_full));
+        ok = mbar_wait(acc_free, static_cast<uint32_t>(i / kSum - 1) & 1u, p.err, KQ_DEV_ERR_TIMEOUT_ACC, p.wait_ns);
+        if (!ok) break;
+        acc = 0;
+      }
       ok = mbar_wait(&full[s], ph, p.err, KQ_DEV_ERR_TIMEOUT_FULL, p.wait_ns);
       if (!ok) break;
       tc_fence_after();
@@ -325,6 +338,7 @@ __global__ void __launch_bounds__(Rows<BT, ACT >= 0, FUSED>::kThreads) k_rows_mm
   uint8_t* tile = ring + (C::kOwnPart ? 0 : C::kPartBytes);             // the ring is read by then
   const bool epi = warp >= 2 && warp < 6;
   bool ok = true;
+  [[maybe_unused]] float sum[C::kProducts][BT];            // LONG
   if (epi || (FUSED && warp > 6)) {
     grid_dep_wait();                                       // bf16 tokens; outputs are written after the grid before
     if (FUSED) {
@@ -335,11 +349,39 @@ __global__ void __launch_bounds__(Rows<BT, ACT >= 0, FUSED>::kThreads) k_rows_mm
     }
   }
   if (epi) {
-    if (GATED && !FUSED && p.out == 2 && blockIdx.x == 0 && rank == 0 && threadIdx.x == 64) *p.oerr = 0u;
-    ok = __all_sync(0xffffffffu, mbar_wait(acc_full, 0, p.err, KQ_DEV_ERR_TIMEOUT_ACC, p.wait_ns));
+    if (GATED && !FUSED && !LONG && p.out == 2 && blockIdx.x == 0 && rank == 0 && threadIdx.x == 64) *p.oerr = 0u;
+    auto come = [&](int piece) {
+      ok = __all_sync(0xffffffffu, mbar_wait(acc_full, static_cast<uint32_t>(piece) & 1u, p.err, KQ_DEV_ERR_TIMEOUT_ACC, p.wait_ns));
+      tc_fence_after();
+      return ok;
+    };
+    if constexpr (LONG) {
+      for (int k = 0; k * kSum < n_kt && come(k); ++k) {
+#pragma unroll
+        for (int j = 0; j < C::kProducts; ++j) add_columns<BT>(tb + 64 * j, k > 0, sum[j]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_free);
+      }
+    } else {
+      come(0);
+    }
     if (!ok) *bad = 1u;
-    tc_fence_after();
   }
+  // 16 tokens of this thread's feature, from token c on
+  auto take = [&](int c, uint32_t (&r)[C::kProducts][16]) {
+#pragma unroll
+    for (int j = 0; j < C::kProducts; ++j) {
+      if constexpr (LONG) {
+#pragma unroll
+        for (int t = 0; t < 16; ++t) r[j][t] = __float_as_uint(sum[j][c + t]);
+      } else {
+        tmem_ld_32x32b_x16(tb + 64 * j + c, r[j]);
+      }
+    }
+    if constexpr (!LONG) tmem_ld_wait();
+  };
+  constexpr int kUnroll = LONG ? BT / 16 : 1;              // registers are not indexed
   if (splits > 1) {
     // tokens go by fours; the share of split d: fours [Q d / splits, Q (d + 1) / splits)
     const int Q = (tokens + 3) / 4, cap = (Q + splits - 1) / splits;
@@ -350,11 +392,11 @@ __global__ void __launch_bounds__(Rows<BT, ACT >= 0, FUSED>::kThreads) k_rows_mm
       const uint32_t mine = smem_u32(part) + 16u * static_cast<uint32_t>(rank * C::kProducts * cap * 128 + 32 * q + lane);
       int d = 0, q0 = 0, q1 = Q / splits;
       uint32_t at = mapa_shared(mine, 0);
-      for (int c = 0; c < tokens; c += 16) {
+#pragma unroll kUnroll
+      for (int c = 0; c < (LONG ? BT : tokens); c += 16) {
+        if (LONG && c >= tokens) break;
         uint32_t r[C::kProducts][16];
-#pragma unroll
-        for (int j = 0; j < C::kProducts; ++j) tmem_ld_32x32b_x16(tb + 64 * j + c, r[j]);
-        tmem_ld_wait();
+        take(c, r);
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           const int four = c / 4 + t;
@@ -392,22 +434,22 @@ __global__ void __launch_bounds__(Rows<BT, ACT >= 0, FUSED>::kThreads) k_rows_mm
               v[j][4 * f] += w.x; v[j][4 * f + 1] += w.y; v[j][4 * f + 2] += w.z; v[j][4 * f + 3] += w.w;
             }
         if (GATED) gate<ACT, 4 * F>(p.out, v[0], v[C::kProducts - 1], v[0]);
-        store<4 * F, GATED && !FUSED>(p, v[0], 4 * four, ok ? min(min(4 * F, 4 * (qe - four)), tokens - 4 * four) : 0, n0, q, lane, top, tile, bad);
+        store<4 * F, GATED && !FUSED && !LONG>(p, v[0], 4 * four, ok ? min(min(4 * F, 4 * (qe - four)), tokens - 4 * four) : 0, n0, q, lane, top, tile, bad);
       }
     }
   } else if (epi) {
-    for (int c = 0; c < tokens; c += 16) {
+#pragma unroll kUnroll
+    for (int c = 0; c < (LONG ? BT : tokens); c += 16) {
+      if (LONG && c >= tokens) break;
       uint32_t r[C::kProducts][16];
-#pragma unroll
-      for (int j = 0; j < C::kProducts; ++j) tmem_ld_32x32b_x16(tb + 64 * j + c, r[j]);
-      tmem_ld_wait();
+      take(c, r);
       float v[C::kProducts][16];
 #pragma unroll
       for (int j = 0; j < C::kProducts; ++j)
 #pragma unroll
         for (int t = 0; t < 16; ++t) v[j][t] = __uint_as_float(r[j][t]);
       if (GATED) gate<ACT, 16>(p.out, v[0], v[C::kProducts - 1], v[0]);
-      store<16, GATED && !FUSED>(p, v[0], c, ok ? min(16, tokens - c) : 0, n0, q, lane, top, tile, bad);
+      store<16, GATED && !FUSED && !LONG>(p, v[0], c, ok ? min(16, tokens - c) : 0, n0, q, lane, top, tile, bad);
     }
   }
   tc_fence_before();
@@ -452,7 +494,10 @@ int max_clusters(int s, int device) {
   cudaLaunchConfig_t cfg = rows_config<BT, ACT >= 0, FUSED>(p, s, attr, nullptr);
   cfg.attrs = attr + 1;
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, k_rows_mm<BT, ACT, FUSED>, &cfg) != cudaSuccess) {
+  auto fn = k_rows_mm<BT, ACT, FUSED, false>;
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(cfg.dynamicSmemBytes)) !=
+          cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) {
     cudaGetLastError();
     n = 0;
   }
@@ -476,12 +521,13 @@ int rows_splits(int64_t tiles, int64_t kt, int sms, int device) {
 template <int BT, int ACT, bool FUSED>
 bool try_rows(const MmParams& p, const Device& d, cudaStream_t st, cudaError_t* e) {
   using C = Rows<BT, ACT >= 0, FUSED>;
-  auto fn = k_rows_mm<BT, ACT, FUSED>;
+  const int64_t kt = cdiv(p.K, kBlk);
+  const int splits = rows_splits<BT, ACT, FUSED>(cdiv(p.N, 128), kt, d.sms, d.device);
+  auto fn = k_rows_mm<BT, ACT, FUSED, false>;
+  if (!FUSED && p.out == 0 && cdiv(kt, splits) > sum_tiles(ACT >= 0)) fn = k_rows_mm<BT, ACT, FUSED, !FUSED>;
   *e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                             static_cast<int>(C::smem(FUSED ? C::kMaxShare : 0)));
   if (*e != cudaSuccess) return true;
-  const int64_t kt = cdiv(p.K, kBlk);
-  const int splits = rows_splits<BT, ACT, FUSED>(cdiv(p.N, 128), kt, d.sms, d.device);
   // Encoding on the way in adds 0.8 us to the product for 4 blocks of a CTA, 1.3 for 32, 1.7 for 64
   // and 2.5 for 128 (512 -> 512, 1 to 32 tokens), a kernel of its own 1.6 and a launch, which costs
   // the host more than 2 us: one round of blocks at most.

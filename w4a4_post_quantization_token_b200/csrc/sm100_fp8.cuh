@@ -163,6 +163,19 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
       : "r"(taddr));
 }
 
+// W columns of this thread's TMEM lane from `col` on: added to v where `more`, else v itself.
+template <int W>
+__device__ __forceinline__ void add_columns(uint32_t col, bool more, float* v) {
+#pragma unroll
+  for (int c = 0; c < W; c += 16) {
+    uint32_t r[16];
+    tmem_ld_32x32b_x16(col + c, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[c + i] = __uint_as_float(r[i]) + (more ? v[c + i] : 0.f);
+  }
+}
+
 // kind::mxf8f6f4 (block32): E4M3 A/B, E8M0 scales, K = 32 per instruction, both K-major.
 // sf_id selects the byte (0 .. 3) of the 32-bit TMEM scale column of A and of B.
 __host__ __device__ constexpr uint32_t idesc_mxf8(uint32_t M, uint32_t N, uint32_t sf_id) {
