@@ -829,3 +829,45 @@ def test_a_wait_that_runs_out_in_a_long_sum(cuda_device, how, M, K, N, ks):
         assert status == kq.ERR_DEVICE_TIMEOUT and seconds < 2
         for s, w in zip(short, whole):
             assert bool((s == 0xAA).all()) and not bool((w == s).all())
+
+
+@pytest.mark.parametrize("kind,M,K,N", [(None, 4096, 256, 9216), (None, 2300, 96, 9600), (None, 3000, 288, 6160), (None, 2600, 12320, 9216),
+                                        ("silu", 4096, 256, 4608), ("gelu", 2300, 96, 4112), ("silu", 1100, 8224, 9600)])
+def test_accumulators_change_hands(cuda_device, kind, M, K, N):
+    """Many tiles for each CTA pair with fp32 outputs, the epilogue that stores most, next to short sums, so
+    that MMAs wait for accumulators to be read: every output right, and alike in 40 runs."""
+    import torch
+    import w4a4_post_quantization_token_b200 as kq
+    L = kq.Fp8Layer(K, N, gated=kind is not None, activation=kind or "silu")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(K)
+    w, act = buf(kq.fp8_weights_bytes(L)), buf(kq.fp8_act_bytes(K, M))
+    Ws = [(torch.randn(K, N, generator=g, device="cuda") / K ** 0.5).bfloat16() for _ in range(1 + L.gated)]
+    kq.fp8_prepare_weights(L, Ws[0], w, Ws[1] if L.gated else None)
+    kq.fp8_quantize_act(torch.randn(M, K, generator=g, device="cuda").bfloat16(), act)
+    A = torch.empty(M, K, device="cuda")
+    kq.fp8_act_unpack(K, act, M, values=A)
+    ns = -(-N // 128) * -(-K // 128)
+    parts = [buf(N * K), buf(ns), buf(N * K), buf(ns)]
+    kq.fp8_weights_unpack(L, w, *parts[:2 + 2 * L.gated])
+    z, acc = [], []
+    for c, s in (parts[:2], parts[2:])[:1 + L.gated]:
+        V = c.view(torch.float8_e4m3fn).view(N, K).double()
+        V *= torch.exp2(s.double() - 127).view(-(-N // 128), -1).repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K]
+        z.append(A.double() @ V.T)
+        acc.append((K / 32 + 2) * 2.0 ** -23 * (A.double().abs() @ V.abs().T))
+    ref, bound = z[0], acc[0]
+    if L.gated:                                             # gated_bound, on the device
+        a = z[0] * torch.sigmoid(z[0]) if kind == "silu" else 0.5 * z[0] * torch.erfc(-z[0] / 2 ** 0.5)
+        ref = a * z[1]
+        bound = 1.13 * acc[0] * (z[1].abs() + acc[1]) + a.abs() * acc[1] + 2.0 ** -19 * a.abs() * z[1].abs()
+    bound = HALF["f32"] * (ref.abs() + bound) + bound + 1e-37
+    want = torch.full((M, N), float("nan"), device="cuda")
+    kq.fp8_gemm(L, w, act, M, want)
+    assert bool(((want.double() - ref).abs() <= bound).all())
+    Y = torch.empty_like(want)
+    for _ in range(40):
+        Y.fill_(float("nan"))
+        kq.fp8_gemm(L, w, act, M, Y)
+        assert torch.equal(Y, want)
+    assert kq.fp8_last_device_error(act) == 0

@@ -104,9 +104,11 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
                : "memory");
 }
 
-// Arrive on a barrier of any CTA of the cluster (a shared::cluster address). Relaxed: it orders
-// nothing but what the caller has waited for (TMEM loads); a release would wait for this
-// thread's stores to global memory too.
+// Arrive on a barrier of any CTA of the cluster (a shared::cluster address). Relaxed, since it passes on
+// TMEM columns and no memory: the loads from them have ended (tcgen05.wait::ld), and the fences
+// tcgen05.fence::before_thread_sync ahead of it and ::after_thread_sync behind the wait order them
+// before the MMAs that follow there, which is what the PTX ISA asks of tcgen05 operations of
+// different threads. A release would wait for this thread's stores to global memory too.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
