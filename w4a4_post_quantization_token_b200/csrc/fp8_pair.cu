@@ -27,10 +27,11 @@
 // Where tiles are fewer than pairs of SMs, two or four pairs share K and exchange partial sums as in
 // k_rows_mm (SPLIT).
 //
-// Bound by the tensor pipe and, repeated, by the power cap: 8192^3 366 us (3.0 PFLOP/s, nine tenths of
-// twice the measured bf16 rate) in bursts, 431 us repeated at 1.2 GHz; 4096 x 1152 -> 4608 20.2 us
-// (2.15 PFLOP/s), where set-up, the pause between tiles and the last epilogue are half the time;
-// gated 4096 x 4096 -> 12288 285 us (2.9 PFLOP/s).
+// Bound by the tensor pipe and, repeated, by the power cap: 8192^3 361 us (3.0 PFLOP/s, nine tenths of
+// twice the measured bf16 rate) in bursts, 431 us repeated at 1.2 GHz; 4096 x 1152 -> 4608 20.0 us
+// (2.2 PFLOP/s), where set-up, the pause between tiles and the last epilogue are half the time;
+// gated 4096 x 4096 -> 12288 273 us (3.0 PFLOP/s), with GELU 287. With few k-tiles GELU's epilogue,
+// erfc for 64 values a thread, takes longer than the MMAs: 4096 x 1152 -> 4608 35 us, with GELU 72.
 #include <cuda_bf16.h>
 
 #include <atomic>

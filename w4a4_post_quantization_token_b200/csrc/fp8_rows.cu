@@ -35,9 +35,9 @@
 // store, and it adds them in the order of the splits, so results do not vary from run to run.
 //
 // Bound by HBM, or L2 where the weights are there, between fixed costs of some 4 us (launch, set-up,
-// the first load's latency, exchange and epilogue): one token 12288 -> 12288 25.2 us (151 MB, 6.0
-// TB/s; 64 tokens 28.1), gated 8 tokens 4096 -> 12288 18.6 us (101 MB, 5.4 TB/s), one token 4096 ->
-// 4096 with the weights in L2 4.5 us, 512 -> 512 2.1 us.
+// the first load's latency, exchange and epilogue): one token 12288 -> 12288 25.3 us (151 MB, 6.0
+// TB/s; 64 tokens 27.3), gated 8 tokens 4096 -> 12288 18.2 us (101 MB, 5.5 TB/s), one token 4096 ->
+// 4096 with the weights in L2 4.7 us, 512 -> 512 2.2 us.
 #include <cuda_bf16.h>
 
 #include <atomic>
